@@ -20,7 +20,7 @@ INCLUDE = os.path.join(_ROOT, "include")
 BUILD = os.path.join(_PKG, "_build")
 LIB = os.path.join(BUILD, "libhs.so")
 SOURCES = ("api.cu", "hostmem.cu", "resolve.cu", "copy.cu", "noalloc.cu", "attention.cu",
-           "attention_heads.cu")
+           "attention_heads.cu", "qk_norm_rope.cu", "group_attention.cu", "select_heavy.cu")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 _lock = threading.Lock()
@@ -134,13 +134,23 @@ class LayerState(ctypes.Structure):
                 ("resolves", ctypes.c_void_p)]
 
 
+class QkDesc(ctypes.Structure):
+    _fields_ = [("q_heads", ctypes.c_int32), ("heads", ctypes.c_int32),
+                ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("q_stride", ctypes.c_int64),
+                ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
+                ("inv_freq", ctypes.c_double * 64)]
+
+
 EXPORTS = ("hs_create_pool", "hs_destroy_pool", "hs_host_records", "hs_device_views",
            "hs_pool_info", "hs_device_host_numa", "hs_touch_records", "hs_warm_pool",
            "hs_resolve", "hs_resolve_anchor", "hs_resolve_measure", "hs_measure_stamp_slots", "hs_plan_bytes",
            "hs_prefetch_plan", "hs_prefetch_copy",
            "hs_stats", "hs_reset", "hs_link_probe", "hs_kernels_per_call", "hs_strerror",
            "hs_resolve_noalloc", "hs_sparse_attention", "hs_sparse_attention_heads",
-           "hs_attention_status")
+           "hs_attention_status", "hs_qk_norm_rope", "hs_prefix_attention_bytes",
+           "hs_prefix_attention", "hs_attention_weights_bytes", "hs_sparse_attention_weights",
+           "hs_select_heavy")
 
 
 def _declare(lib):
@@ -174,6 +184,16 @@ def _declare(lib):
                                 ctypes.c_int),
         "hs_sparse_attention_heads": ([vp, vp, i64, vp, i32, i32, i32, ctypes.c_float, vp, vp],
                                       ctypes.c_int),
+        "hs_qk_norm_rope": ([ctypes.POINTER(QkDesc), vp, vp, vp, vp, vp, vp, i32, vp, vp, i64, vp,
+                             vp], ctypes.c_int),
+        "hs_prefix_attention_bytes": ([i32, i32, i32, i64, i32], ctypes.c_size_t),
+        "hs_prefix_attention": ([vp, vp, i64, vp, i64, vp, i32, i32, i32, i32, ctypes.c_float, vp,
+                                 vp, ctypes.c_size_t, vp], ctypes.c_int),
+        "hs_attention_weights_bytes": ([i32, i32, i32, i32], ctypes.c_size_t),
+        "hs_sparse_attention_weights": ([vp, vp, i64, vp, vp, vp, i32, i32, i32, i32,
+                                         ctypes.c_float, vp, vp, i32, i64, vp, ctypes.c_size_t,
+                                         vp], ctypes.c_int),
+        "hs_select_heavy": ([vp, i32, i64, vp, vp, i32, i32, i32, vp, vp], ctypes.c_int),
         "hs_attention_status": ([ctypes.POINTER(ctypes.c_uint32)], ctypes.c_int),
     }
     for name, (args, res) in sig.items():

@@ -2,6 +2,7 @@
 // argument checks, launches, counters and the link probe.
 #include <algorithm>
 #include <chrono>
+#include <cmath>
 #include <cstdint>
 #include <cstdlib>
 #include <cstring>
@@ -141,6 +142,16 @@ bool check_common(const hs_pool *p, int32_t layer, int32_t n_req, int32_t k) {
 
 // int32 arrays are read and written with 4-byte accesses
 bool misaligned4(const void *a) { return (reinterpret_cast<uintptr_t>(a) & 3u) != 0; }
+bool misaligned16(const void *a) { return (reinterpret_cast<uintptr_t>(a) & 15u) != 0; }
+
+// per-head token records: up to 8 key-value heads, up to 128 query heads, and
+// for attention the same number of query heads (up to 16) to each of them
+bool head_layout_ok(int32_t q_heads, int32_t heads) {
+    return heads >= 1 && heads <= 8 && q_heads >= 1 && q_heads <= 128;
+}
+bool group_layout_ok(int32_t q_heads, int32_t heads) {
+    return head_layout_ok(q_heads, heads) && q_heads % heads == 0 && q_heads / heads <= 16;
+}
 
 }  // namespace
 
@@ -519,6 +530,160 @@ int hs_attention_status(uint32_t *status) {
     if (!status) return HS_ERR_INVALID_ARG;
     if (!cuda_ok(cudaDeviceSynchronize())) return HS_ERR_CUDA;
     return cuda_ok(hs::attention_status(status)) ? HS_OK : HS_ERR_CUDA;
+}
+
+int hs_qk_norm_rope(const hs_qk_desc *desc, const void *d_q, const void *d_k, const void *d_v,
+                    const void *d_wq, const void *d_wk, const int32_t *d_pos, int32_t n_tok,
+                    void *d_q_out, void *d_records, int64_t record_rows, const int64_t *d_rows,
+                    void *stream) {
+    if (!desc) return HS_ERR_INVALID_ARG;
+    const hs_qk_desc &d = *desc;
+    if (!head_layout_ok(d.q_heads, d.heads) || d.rot_dim < 0 || d.rot_dim > 128 ||
+        d.rot_dim % 16 != 0 || (d.interleaved != 0 && d.interleaved != 1) || !(d.eps >= 0.f) ||
+        !std::isfinite(d.eps) || n_tok < 0 || record_rows < 1)
+        return HS_ERR_INVALID_ARG;
+    hs::QkArgs a = {};
+    const int64_t width[3] = {(int64_t)d.q_heads * 128, (int64_t)d.heads * 128,
+                              (int64_t)d.heads * 128};
+    const int64_t given[3] = {d.q_stride, d.k_stride, d.v_stride};
+    int64_t stride[3];
+    for (int i = 0; i < 3; ++i) {
+        stride[i] = given[i] ? given[i] : width[i];
+        // a token's bytes stay within a 63-bit offset for any 31-bit token count
+        if (stride[i] < width[i] || stride[i] % 8 != 0 || stride[i] > (INT64_MAX >> 34))
+            return HS_ERR_INVALID_ARG;
+    }
+    if (record_rows > INT64_MAX / (d.heads * 512)) return HS_ERR_INVALID_ARG;
+    if (!d_q || !d_k || !d_v || !d_q_out || !d_records || (d.rot_dim && !d_pos) ||
+        misaligned16(d_q) || misaligned16(d_k) || misaligned16(d_v) || misaligned16(d_wq) ||
+        misaligned16(d_wk) || misaligned16(d_q_out) || misaligned16(d_records) ||
+        misaligned4(d_pos) || (reinterpret_cast<uintptr_t>(d_rows) & 7u))
+        return HS_ERR_INVALID_ARG;
+    for (int i = 0; i < d.rot_dim / 2; ++i) {
+        const double turns = d.inv_freq[i] / 6.283185307179586476925287;
+        if (!(std::fabs(turns) < 9007199254740992.0)) return HS_ERR_INVALID_ARG;
+        const double frac = turns - std::floor(turns);  // [0, 1]; 1 where a tiny negative rounds up
+        a.freq[i] = frac < 1.0 ? (uint64_t)std::ldexp(frac, 64) : 0;
+    }
+    if (n_tok == 0) return HS_OK;
+    a.q = static_cast<const uint8_t *>(d_q);
+    a.k = static_cast<const uint8_t *>(d_k);
+    a.v = static_cast<const uint8_t *>(d_v);
+    a.wq = static_cast<const uint8_t *>(d_wq);
+    a.wk = static_cast<const uint8_t *>(d_wk);
+    a.q_stride = stride[0];
+    a.k_stride = stride[1];
+    a.v_stride = stride[2];
+    a.pos = d_pos;
+    a.rows = d_rows;
+    a.q_out = static_cast<uint8_t *>(d_q_out);
+    a.records = static_cast<uint8_t *>(d_records);
+    a.record_rows = record_rows;
+    a.n_tok = n_tok;
+    a.q_heads = d.q_heads;
+    a.heads = d.heads;
+    a.rot_dim = d.rot_dim;
+    a.interleaved = d.interleaved;
+    a.eps = d.eps;
+    return cuda_ok(hs::launch_qk_norm_rope(a, static_cast<cudaStream_t>(stream))) ? HS_OK
+                                                                                 : HS_ERR_CUDA;
+}
+
+size_t hs_prefix_attention_bytes(int32_t n_req, int32_t q_heads, int32_t heads,
+                                 int64_t prefix_len, int32_t k) {
+    if (n_req < 1 || n_req > 65535 || !group_layout_ok(q_heads, heads) || prefix_len < 1 ||
+        prefix_len > INT32_MAX || k < 0)
+        return 0;
+    return hs::prefix_attention_bytes(n_req, q_heads, heads, prefix_len, k);
+}
+
+int hs_prefix_attention(const void *d_q, const void *d_prefix, int64_t prefix_len,
+                        const void *d_cache, int64_t cache_rows, const int32_t *d_idx,
+                        int32_t n_req, int32_t k, int32_t q_heads, int32_t heads, float scale,
+                        void *d_out, void *d_work, size_t work_bytes, void *stream) {
+    if (!d_q || !d_out || n_req < 0 || n_req > 65535 || k < 0 || prefix_len < 0 ||
+        prefix_len > INT32_MAX || !group_layout_ok(q_heads, heads) || misaligned16(d_q) ||
+        misaligned16(d_out) || misaligned16(d_work) || (prefix_len > 0 && !d_prefix) ||
+        misaligned16(d_prefix))
+        return HS_ERR_INVALID_ARG;
+    if (k > 0 && (!d_cache || !d_idx || cache_rows < 1)) return HS_ERR_INVALID_ARG;
+    if (misaligned16(d_cache) || misaligned4(d_idx)) return HS_ERR_INVALID_ARG;
+    const size_t need = hs_prefix_attention_bytes(n_req, q_heads, heads, prefix_len, k);
+    if (need > work_bytes || (need && !d_work)) return HS_ERR_INVALID_ARG;
+    if (n_req == 0) return HS_OK;
+    hs::GroupArgs a = {};
+    a.q = static_cast<const uint8_t *>(d_q);
+    a.prefix = static_cast<const uint8_t *>(d_prefix);
+    a.prefix_len = prefix_len;
+    a.cache = static_cast<const uint8_t *>(d_cache);
+    a.cache_rows = cache_rows;
+    a.idx = d_idx;
+    a.n_req = n_req;
+    a.k = k;
+    a.q_heads = q_heads;
+    a.heads = heads;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    a.out = static_cast<uint8_t *>(d_out);
+    return cuda_ok(hs::launch_prefix_attention(a, d_work, static_cast<cudaStream_t>(stream)))
+               ? HS_OK
+               : HS_ERR_CUDA;
+}
+
+size_t hs_attention_weights_bytes(int32_t n_req, int32_t q_heads, int32_t heads, int32_t k) {
+    if (n_req < 1 || n_req > 65535 || !group_layout_ok(q_heads, heads) || k < 1) return 0;
+    return hs::attention_weights_bytes(n_req, q_heads, heads, k);
+}
+
+int hs_sparse_attention_weights(const void *d_q, const void *d_cache, int64_t cache_rows,
+                                const int32_t *d_idx, const int32_t *d_sel,
+                                const int32_t *d_req_ids, int32_t n_req, int32_t k,
+                                int32_t q_heads, int32_t heads, float scale, void *d_out,
+                                float *d_weights, int32_t weight_rows, int64_t n_positions,
+                                void *d_work, size_t work_bytes, void *stream) {
+    if (!d_q || !d_cache || !d_idx || !d_sel || !d_out || !d_weights || cache_rows < 1 ||
+        n_req < 0 || n_req > 65535 || k < 1 || !group_layout_ok(q_heads, heads) ||
+        weight_rows < 1 || n_positions < 1 || n_positions > INT32_MAX || misaligned16(d_q) ||
+        misaligned16(d_cache) || misaligned16(d_out) || misaligned16(d_work) ||
+        misaligned4(d_idx) || misaligned4(d_sel) || misaligned4(d_req_ids) ||
+        misaligned4(d_weights))
+        return HS_ERR_INVALID_ARG;
+    const size_t need = hs_attention_weights_bytes(n_req, q_heads, heads, k);
+    if (need > work_bytes || (need && !d_work)) return HS_ERR_INVALID_ARG;
+    if (n_req == 0) return HS_OK;
+    hs::GroupArgs a = {};
+    a.q = static_cast<const uint8_t *>(d_q);
+    a.cache = static_cast<const uint8_t *>(d_cache);
+    a.cache_rows = cache_rows;
+    a.idx = d_idx;
+    a.n_req = n_req;
+    a.k = k;
+    a.q_heads = q_heads;
+    a.heads = heads;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    a.out = static_cast<uint8_t *>(d_out);
+    a.weights = d_weights;
+    a.weight_rows = weight_rows;
+    a.n_positions = n_positions;
+    a.sel = d_sel;
+    a.req_ids = d_req_ids;
+    return cuda_ok(hs::launch_attention_weights(a, d_work, static_cast<cudaStream_t>(stream)))
+               ? HS_OK
+               : HS_ERR_CUDA;
+}
+
+int hs_select_heavy(const float *d_weights, int32_t weight_rows, int64_t n_positions,
+                    const int32_t *d_req_ids, const int32_t *d_len, int32_t n_req, int32_t k,
+                    int32_t recent, int32_t *d_sel, void *stream) {
+    if (!d_weights || !d_sel || weight_rows < 1 || n_positions < 1 || n_positions > INT32_MAX ||
+        n_req < 0 || n_req > 65535 || k < 1 || recent < 0 || recent > k ||
+        misaligned4(d_weights) || misaligned4(d_req_ids) || misaligned4(d_len) ||
+        misaligned4(d_sel))
+        return HS_ERR_INVALID_ARG;
+    if (n_req == 0) return HS_OK;
+    hs::SelectArgs a = {d_weights, weight_rows, n_positions, d_req_ids, d_len, k, recent, d_sel};
+    return cuda_ok(hs::launch_select_heavy(a, n_req, static_cast<cudaStream_t>(stream)))
+               ? HS_OK
+               : HS_ERR_CUDA;
 }
 
 int hs_link_probe(size_t bytes, int32_t reps, int32_t record_bytes, int32_t host_alloc,

@@ -235,7 +235,8 @@ int device_host_numa(int dev);
 void host_free(HostBuffer *b);
 int page_numa_node(const void *addr);
 
-// launchers (resolve.cu, copy.cu, attention.cu, attention_heads.cu)
+// launchers (resolve.cu, copy.cu, attention.cu, attention_heads.cu, and
+// further down qk_norm_rope.cu, group_attention.cu, select_heavy.cu)
 // plan_layer: a consumed plan may carry this layer id besides `layer` (the
 // anchor whose resolve wrote it); plan_out: where an anchor's resolve
 // writes its own miss plan (NULL: nowhere); overlap: the launch may start
@@ -269,6 +270,53 @@ cudaError_t attention_status(uint32_t *status);
 cudaError_t launch_attention_heads(const void *q, const void *cache, int64_t cache_rows,
                                    const int32_t *idx, int n_req, int k, int heads, float scale,
                                    float *out, cudaStream_t st);
+
+// qk_norm_rope.cu: hs_qk_norm_rope (fields as in hs.h; strides in elements)
+struct QkArgs {
+    const uint8_t *q, *k, *v, *wq, *wk;
+    int64_t q_stride, k_stride, v_stride;
+    const int32_t *pos;
+    const int64_t *rows;
+    uint8_t *q_out, *records;
+    int64_t record_rows;
+    int32_t n_tok, q_heads, heads, rot_dim, interleaved;
+    float eps;
+    uint64_t freq[64];  // inv_freq / 2 pi as a 64-bit fraction of a turn
+};
+cudaError_t launch_qk_norm_rope(const QkArgs &a, cudaStream_t st);
+
+// group_attention.cu: hs_prefix_attention, hs_sparse_attention_weights
+struct GroupArgs {
+    const uint8_t *q, *prefix, *cache;
+    int64_t prefix_len, cache_rows;
+    const int32_t *idx;
+    int32_t n_req, k, q_heads, heads;
+    float scale_log2;
+    uint8_t *out;
+    // weights only
+    float *weights;  // NULL: none
+    int32_t weight_rows;
+    int64_t n_positions;
+    const int32_t *sel, *req_ids;
+    float2 *ml;      // [n_req][q_heads] maximum (base 2) and 1 / sum
+    float *scores;   // [n_req][q_heads][k]
+};
+size_t prefix_attention_bytes(int n_req, int q_heads, int heads, int64_t prefix_len, int k);
+size_t attention_weights_bytes(int n_req, int q_heads, int heads, int k);
+cudaError_t launch_prefix_attention(GroupArgs a, void *work, cudaStream_t st);
+cudaError_t launch_attention_weights(GroupArgs a, void *work, cudaStream_t st);
+
+// select_heavy.cu: hs_select_heavy
+struct SelectArgs {
+    const float *weights;
+    int32_t weight_rows;
+    int64_t n_positions;
+    const int32_t *req_ids, *len;
+    int32_t k, recent;
+    int32_t *sel;
+};
+cudaError_t launch_select_heavy(const SelectArgs &a, int n_req, cudaStream_t st);
+
 cudaError_t launch_gather_probe(const uint8_t *src, uint8_t *dst, const int32_t *idx,
                                 int64_t n_rec, int W, int sm_count, cudaStream_t st);
 

@@ -236,6 +236,79 @@ def hs_attention_status() -> int:
     return int(v.value)
 
 
+def qk_desc(q_heads, heads, inv_freq, eps=1e-6, interleaved=False, q_stride=0, k_stride=0,
+            v_stride=0) -> _native.QkDesc:
+    """Descriptor of hs_qk_norm_rope: len(inv_freq) pairs are rotated
+    (rot_dim = 2 * len(inv_freq)); strides in elements between tokens (0:
+    dense)."""
+    freq = [float(f) for f in inv_freq]
+    if len(freq) > 64:
+        raise ValueError("at most 64 rotated pairs in a head of 128")
+    return _native.QkDesc(q_heads, heads, 2 * len(freq), int(interleaved), eps, q_stride,
+                          k_stride, v_stride, (ctypes.c_double * 64)(*freq))
+
+
+def hs_qk_norm_rope(desc, q, k, v, wq, wk, pos, n_tok, q_out, records, record_rows, rows=None,
+                    stream=None) -> None:
+    """Per-head RMS norm (weights wq, wk: bf16 [128] or None) and position
+    rotation of n_tok tokens' queries and keys; q_out bf16
+    [n_tok][q_heads][128], and each token's record (keys, then the values as
+    they are) into row rows[i] (int64; None: row i) of `records`.  `desc` is
+    a qk_desc."""
+    _check(_lib().hs_qk_norm_rope(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(wq),
+                                  _ptr(wk), _ptr(pos), n_tok, _ptr(q_out), _ptr(records),
+                                  record_rows, _ptr(rows), _stream(stream)), "hs_qk_norm_rope")
+
+
+def hs_prefix_attention_bytes(n_req: int, q_heads: int, heads: int, prefix_len: int,
+                              k: int) -> int:
+    """Workspace bytes of hs_prefix_attention (0: none needed)."""
+    return int(_lib().hs_prefix_attention_bytes(n_req, q_heads, heads, prefix_len, k))
+
+
+def hs_prefix_attention(q, prefix, prefix_len, cache, cache_rows, idx, n_req, k, q_heads, heads,
+                        scale, out, work=None, work_bytes=0, stream=None) -> None:
+    """Attention of q [n_req][q_heads][128] bf16 over prefix_len token records
+    that all requests share and over each request's published rows idx
+    [n_req][k] of `cache`; bf16 out [n_req][q_heads][128]."""
+    _check(_lib().hs_prefix_attention(_ptr(q), _ptr(prefix), prefix_len, _ptr(cache), cache_rows,
+                                      _ptr(idx), n_req, k, q_heads, heads, scale, _ptr(out),
+                                      _ptr(work), work_bytes, _stream(stream)),
+           "hs_prefix_attention")
+
+
+def hs_attention_weights_bytes(n_req: int, q_heads: int, heads: int, k: int) -> int:
+    """Workspace bytes of hs_sparse_attention_weights (0: none needed)."""
+    return int(_lib().hs_attention_weights_bytes(n_req, q_heads, heads, k))
+
+
+def hs_sparse_attention_weights(q, cache, cache_rows, idx, sel, n_req, k, q_heads, heads, scale,
+                                out, weights, weight_rows, n_positions, work=None, work_bytes=0,
+                                req_ids=None, stream=None) -> None:
+    """Attention of q [n_req][q_heads][128] bf16 over the published rows idx
+    [n_req][k]; bf16 out [n_req][q_heads][128].  Also adds to weights
+    [weight_rows][n_positions] (fp32), at request req_ids[i] (None: i) and
+    position sel[i][j], the attention weight of row j summed over the query
+    heads."""
+    _check(_lib().hs_sparse_attention_weights(_ptr(q), _ptr(cache), cache_rows, _ptr(idx),
+                                              _ptr(sel), _ptr(req_ids), n_req, k, q_heads, heads,
+                                              scale, _ptr(out), _ptr(weights), weight_rows,
+                                              n_positions, _ptr(work), work_bytes,
+                                              _stream(stream)),
+           "hs_sparse_attention_weights")
+
+
+def hs_select_heavy(weights, weight_rows, n_positions, lens, n_req, k, recent, sel, req_ids=None,
+                    stream=None) -> None:
+    """The k positions each request keeps, ascending, into sel [n_req][k]
+    int32: the `recent` last of its lens[i] (None: n_positions) positions and
+    those of the largest weights[req_ids[i]] among the others; -1 past the
+    request's length."""
+    _check(_lib().hs_select_heavy(_ptr(weights), weight_rows, n_positions, _ptr(req_ids),
+                                  _ptr(lens), n_req, k, recent, _ptr(sel), _stream(stream)),
+           "hs_select_heavy")
+
+
 HS_NOALLOC_MAX_REQUESTS = 4096
 
 

@@ -490,6 +490,135 @@ int hs_sparse_attention_heads(const void *d_q, const void *d_cache, int64_t cach
                               const int32_t *d_idx, int32_t n_req, int32_t k, int32_t heads,
                               float scale, float *d_out, void *stream);
 
+/* ---- a decode step over per-head token records ------------------------- */
+
+/* hs_qk_norm_rope's layout and constants.  Read by the call, not kept. */
+typedef struct {
+    int32_t q_heads;      /* query heads of a token (1 .. 128) */
+    int32_t heads;        /* key-value heads of a token (1 .. 8) */
+    int32_t rot_dim;      /* leading dimensions of a head that rotate: a multiple of 16, 0 .. 128 */
+    int32_t interleaved;  /* 0: dimension i turns with i + rot_dim / 2; 1: 2i with 2i + 1 */
+    float eps;            /* >= 0 */
+    /* elements from one token's first query / key / value head to the next
+       token's: a multiple of 8, at least the heads' own width (0: exactly that) */
+    int64_t q_stride, k_stride, v_stride;
+    /* inv_freq[i]: radians per position of pair i, i < rot_dim / 2 */
+    double inv_freq[64];
+} hs_qk_desc;
+
+/*
+ * The queries and token records of n_tok new tokens, in one pass.  Every
+ * query head and every key head x (128 bf16) becomes
+ *   y = x * w / sqrt(mean(x^2) + eps)            (w: d_wq or d_wk, 128 bf16; NULL: ones)
+ * and each pair (a, b) of its first rot_dim dimensions turns by
+ * t = d_pos[i] * inv_freq[pair]: (a cos t - b sin t, a sin t + b cos t).
+ * d_q, d_k, d_v: device bf16, token i's heads at element i * stride (they
+ *   may be parts of one fused projection output).
+ * d_pos: device int32[n_tok], any value (NULL if rot_dim is 0).
+ * d_q_out: device bf16 [n_tok][q_heads][128].
+ * d_records: record_rows rows of heads * 512 bytes (the layout that
+ *   hs_sparse_attention_heads reads): token i's keys as above and its values
+ *   unchanged go to row d_rows[i] (device int64[n_tok]; NULL: row i).  A row
+ *   outside [0, record_rows) writes no record (a padding token; its queries
+ *   are written all the same); rows that no token names stay as they were;
+ *   rows of one call must differ.  The records may be device memory or a
+ *   pool's mapped host records: the layer's records of all requests are one
+ *   range of R * L_ctx rows from hs_host_records(pool, 0, layer), row
+ *   r * L_ctx + pos.  A later launch in the same stream, an overlapping
+ *   resolve too, reads what this call wrote; a record that the pool's slots
+ *   already hold is not refreshed there.
+ * fp32 throughout, one rounding to bf16 at the end; the angle is exact to
+ * 2^-31 of half a turn at any position.  Outputs overlap no input.  All
+ * buffers 16-byte aligned, d_pos 4, d_rows 8.  One kernel, no workspace;
+ * nothing is allocated; n_tok == 0 enqueues nothing.
+ * Errors: HS_ERR_INVALID_ARG, HS_ERR_CUDA.
+ */
+int hs_qk_norm_rope(const hs_qk_desc *desc, const void *d_q, const void *d_k, const void *d_v,
+                    const void *d_wq, const void *d_wk, const int32_t *d_pos, int32_t n_tok,
+                    void *d_q_out, void *d_records, int64_t record_rows, const int64_t *d_rows,
+                    void *stream);
+
+/* Workspace bytes of hs_prefix_attention, the same on every device (0: none
+ * needed, or arguments that the call refuses). */
+size_t hs_prefix_attention_bytes(int32_t n_req, int32_t q_heads, int32_t heads,
+                                 int64_t prefix_len, int32_t k);
+
+/*
+ * Attention of a batch whose requests share a prefix: query head h of
+ * request i attends, with the key-value head h / (q_heads / heads), to the
+ * prefix_len token records of d_prefix and to the request's own published
+ * rows d_cache[d_idx[i][j]], j < k, in one softmax:
+ *   out[i][h] = softmax(scale * q[i][h] . [K_prefix, K_own]) [V_prefix, V_own].
+ * The prefix is read once for the whole batch.  The record layout is that of
+ * hs_sparse_attention_heads (heads * 512 bytes), with 1 to 16 query heads to
+ * a key-value head.  d_q, d_out: device bf16 [n_req][q_heads][128];
+ * d_prefix: prefix_len consecutive rows (NULL if prefix_len is 0); d_cache,
+ * cache_rows, d_idx as there (ignored if k is 0; an index outside
+ * [0, cache_rows) masks its row).  A request with no row at all gets zeros.
+ * d_work: hs_prefix_attention_bytes(...) bytes of device memory (NULL if
+ * that is 0), written and read by this call only: two calls that may run at
+ * once, captured ones too, need one each.  Buffers 16-byte aligned, d_idx 4.
+ * Scores, maxima, sums and outputs are held in fp32; each probability is
+ * rounded once to bf16 for its product with the value, and the output once.
+ * The work split depends on the arguments and the device only, so equal
+ * inputs give bit-identical outputs.  Nothing is allocated; n_req == 0
+ * enqueues nothing; n_req <= 65535, prefix_len < 2^31.
+ * Errors: HS_ERR_INVALID_ARG (also a workspace that is too small),
+ * HS_ERR_CUDA.
+ */
+int hs_prefix_attention(const void *d_q, const void *d_prefix, int64_t prefix_len,
+                        const void *d_cache, int64_t cache_rows, const int32_t *d_idx,
+                        int32_t n_req, int32_t k, int32_t q_heads, int32_t heads, float scale,
+                        void *d_out, void *d_work, size_t work_bytes, void *stream);
+
+/* Workspace bytes of hs_sparse_attention_weights, the same on every device
+ * (0: none needed, or arguments that the call refuses). */
+size_t hs_attention_weights_bytes(int32_t n_req, int32_t q_heads, int32_t heads, int32_t k);
+
+/*
+ * Attention over the published rows that also accumulates how much weight
+ * every position receives, the measure by which hs_select_heavy keeps or
+ * drops it.  out[i][h] as hs_prefix_attention with no prefix; and with
+ * p[i][h][j] the softmax weight of row j,
+ *   d_weights[req][d_sel[i][j]] += sum over h of p[i][h][j],
+ * req = d_req_ids[i], or i when d_req_ids is NULL.
+ * d_sel: device int32 [n_req][k], the positions that the resolve which
+ * published d_idx was given; d_weights: device fp32
+ * [weight_rows][n_positions].  A masked row adds nothing; a position outside
+ * [0, n_positions) or a request id outside [0, weight_rows) only loses its
+ * addition.  Positions of one request should differ (they do in a selection
+ * hs_resolve accepts): a repeated one still receives every addition, in an
+ * order that may vary.  The weights come from fp32 scores and are not
+ * rounded to fewer bits.  d_work: hs_attention_weights_bytes(...) bytes, as
+ * for hs_prefix_attention.  Other arguments, limits, alignment and errors as
+ * there; d_sel, d_req_ids and d_weights 4-byte aligned; k >= 1;
+ * n_positions < 2^31.
+ */
+int hs_sparse_attention_weights(const void *d_q, const void *d_cache, int64_t cache_rows,
+                                const int32_t *d_idx, const int32_t *d_sel,
+                                const int32_t *d_req_ids, int32_t n_req, int32_t k,
+                                int32_t q_heads, int32_t heads, float scale, void *d_out,
+                                float *d_weights, int32_t weight_rows, int64_t n_positions,
+                                void *d_work, size_t work_bytes, void *stream);
+
+/*
+ * The positions a request keeps when the rest of its context is evicted: of
+ * its n = d_len[i] positions (device int32[n_req], taken into
+ * [0, n_positions]; NULL: n_positions) the last min(recent, n), and of the
+ * others those with the largest d_weights[req][pos], min(k, n) in all.
+ * Equal weights go to the lowest position, -0 equals 0, NaN counts as
+ * -infinity.  d_sel[i] (device int32 [n_req][k]) receives them in ascending
+ * order, then -1 up to k: where n >= k it is a selection for hs_resolve.
+ * d_weights, weight_rows, n_positions and d_req_ids as for
+ * hs_sparse_attention_weights; an id outside [0, weight_rows) gives -1
+ * throughout.  0 <= recent <= k.  d_weights is only read; 4-byte alignment.
+ * One kernel, no workspace; nothing is allocated; n_req == 0 enqueues
+ * nothing; n_req <= 65535.  Errors: HS_ERR_INVALID_ARG, HS_ERR_CUDA.
+ */
+int hs_select_heavy(const float *d_weights, int32_t weight_rows, int64_t n_positions,
+                    const int32_t *d_req_ids, const int32_t *d_len, int32_t n_req, int32_t k,
+                    int32_t recent, int32_t *d_sel, void *stream);
+
 /* Kernels launched per call of hs_resolve / hs_prefetch_plan /
  * hs_prefetch_copy (for launch accounting; always 1 in this build). */
 int32_t hs_kernels_per_call(void);
