@@ -20,7 +20,8 @@ INCLUDE = os.path.join(_ROOT, "include")
 BUILD = os.path.join(_PKG, "_build")
 LIB = os.path.join(BUILD, "libhs.so")
 SOURCES = ("api.cu", "hostmem.cu", "resolve.cu", "copy.cu", "noalloc.cu", "attention.cu",
-           "attention_heads.cu", "qk_norm_rope.cu", "group_attention.cu", "select_heavy.cu")
+           "attention_heads.cu", "qk_norm_rope.cu", "group_attention.cu", "prefix_attention.cu",
+           "select_heavy.cu")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 _lock = threading.Lock()

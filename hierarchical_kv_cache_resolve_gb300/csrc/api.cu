@@ -146,6 +146,8 @@ bool misaligned16(const void *a) { return (reinterpret_cast<uintptr_t>(a) & 15u)
 
 // per-head token records: up to 8 key-value heads, up to 128 query heads, and
 // for attention the same number of query heads (up to 16) to each of them
+constexpr int32_t kMaxRows = 1 << 30;  // published rows per request
+
 bool head_layout_ok(int32_t q_heads, int32_t heads) {
     return heads >= 1 && heads <= 8 && q_heads >= 1 && q_heads <= 128;
 }
@@ -529,7 +531,11 @@ int hs_sparse_attention_heads(const void *d_q, const void *d_cache, int64_t cach
 int hs_attention_status(uint32_t *status) {
     if (!status) return HS_ERR_INVALID_ARG;
     if (!cuda_ok(cudaDeviceSynchronize())) return HS_ERR_CUDA;
-    return cuda_ok(hs::attention_status(status)) ? HS_OK : HS_ERR_CUDA;
+    uint32_t mla = 0, prefix = 0;
+    if (!cuda_ok(hs::attention_status(&mla)) || !cuda_ok(hs::prefix_attention_status(&prefix)))
+        return HS_ERR_CUDA;
+    *status = mla | prefix;
+    return HS_OK;
 }
 
 int hs_qk_norm_rope(const hs_qk_desc *desc, const void *d_q, const void *d_k, const void *d_v,
@@ -591,8 +597,8 @@ int hs_qk_norm_rope(const hs_qk_desc *desc, const void *d_q, const void *d_k, co
 
 size_t hs_prefix_attention_bytes(int32_t n_req, int32_t q_heads, int32_t heads,
                                  int64_t prefix_len, int32_t k) {
-    if (n_req < 1 || n_req > 65535 || !group_layout_ok(q_heads, heads) || prefix_len < 1 ||
-        prefix_len > INT32_MAX || k < 0)
+    if (n_req < 1 || n_req > 65535 || !group_layout_ok(q_heads, heads) || prefix_len < 0 ||
+        prefix_len > INT32_MAX || k < 0 || k > kMaxRows)
         return 0;
     return hs::prefix_attention_bytes(n_req, q_heads, heads, prefix_len, k);
 }
@@ -601,8 +607,8 @@ int hs_prefix_attention(const void *d_q, const void *d_prefix, int64_t prefix_le
                         const void *d_cache, int64_t cache_rows, const int32_t *d_idx,
                         int32_t n_req, int32_t k, int32_t q_heads, int32_t heads, float scale,
                         void *d_out, void *d_work, size_t work_bytes, void *stream) {
-    if (!d_q || !d_out || n_req < 0 || n_req > 65535 || k < 0 || prefix_len < 0 ||
-        prefix_len > INT32_MAX || !group_layout_ok(q_heads, heads) || misaligned16(d_q) ||
+    if (!d_q || !d_out || n_req < 0 || n_req > 65535 || k < 0 || k > kMaxRows ||
+        prefix_len < 0 || prefix_len > INT32_MAX || !group_layout_ok(q_heads, heads) || misaligned16(d_q) ||
         misaligned16(d_out) || misaligned16(d_work) || (prefix_len > 0 && !d_prefix) ||
         misaligned16(d_prefix))
         return HS_ERR_INVALID_ARG;
@@ -630,7 +636,9 @@ int hs_prefix_attention(const void *d_q, const void *d_prefix, int64_t prefix_le
 }
 
 size_t hs_attention_weights_bytes(int32_t n_req, int32_t q_heads, int32_t heads, int32_t k) {
-    if (n_req < 1 || n_req > 65535 || !group_layout_ok(q_heads, heads) || k < 1) return 0;
+    if (n_req < 1 || n_req > 65535 || !group_layout_ok(q_heads, heads) || k < 1 ||
+        k > kMaxRows)
+        return 0;
     return hs::attention_weights_bytes(n_req, q_heads, heads, k);
 }
 
@@ -641,7 +649,7 @@ int hs_sparse_attention_weights(const void *d_q, const void *d_cache, int64_t ca
                                 float *d_weights, int32_t weight_rows, int64_t n_positions,
                                 void *d_work, size_t work_bytes, void *stream) {
     if (!d_q || !d_cache || !d_idx || !d_sel || !d_out || !d_weights || cache_rows < 1 ||
-        n_req < 0 || n_req > 65535 || k < 1 || !group_layout_ok(q_heads, heads) ||
+        n_req < 0 || n_req > 65535 || k < 1 || k > kMaxRows || !group_layout_ok(q_heads, heads) ||
         weight_rows < 1 || n_positions < 1 || n_positions > INT32_MAX || misaligned16(d_q) ||
         misaligned16(d_cache) || misaligned16(d_out) || misaligned16(d_work) ||
         misaligned4(d_idx) || misaligned4(d_sel) || misaligned4(d_req_ids) ||

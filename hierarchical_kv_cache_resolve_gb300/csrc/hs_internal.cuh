@@ -298,13 +298,34 @@ struct GroupArgs {
     int32_t weight_rows;
     int64_t n_positions;
     const int32_t *sel, *req_ids;
-    float2 *ml;      // [n_req][q_heads] maximum (base 2) and 1 / sum
-    float *scores;   // [n_req][q_heads][k]
+    float *scores;   // [n_req][q_heads][k], base 2, -inf where masked
+};
+constexpr int kSms = 152;  // the SMs that work is split over, whatever device asks
+
+// Parts of a softmax: unnormalised outputs o[part][...][128] and
+// ml[part][...] = (maximum, base 2; sum).  A split of the published rows:
+// ctas ranges of the n_req * tiles tiles, each taken in subs turns; the part
+// of (CTA c, request r, turn s) is (c + r) * subs + s, of q_heads rows.
+struct RowsPlan {
+    int32_t tiles, subs, ctas;
+    int64_t total;
+    float *o;
+    float2 *ml;
+};
+// A split of the prefix: part s holds n_req * q_heads rows.
+struct PrefixPlan {
+    int32_t splits, blocks, row_tiles;
+    float *o;
+    float2 *ml;
 };
 size_t prefix_attention_bytes(int n_req, int q_heads, int heads, int64_t prefix_len, int k);
 size_t attention_weights_bytes(int n_req, int q_heads, int heads, int k);
 cudaError_t launch_prefix_attention(GroupArgs a, void *work, cudaStream_t st);
 cudaError_t launch_attention_weights(GroupArgs a, void *work, cudaStream_t st);
+// prefix_attention.cu
+PrefixPlan prefix_plan(int n_req, int q_heads, int heads, int64_t prefix_len);
+cudaError_t launch_prefix(const GroupArgs &a, const PrefixPlan &p, cudaStream_t st);
+cudaError_t prefix_attention_status(uint32_t *status);
 
 // select_heavy.cu: hs_select_heavy
 struct SelectArgs {

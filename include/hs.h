@@ -460,8 +460,8 @@ int hs_sparse_attention(const void *d_q, const void *d_cache, int64_t cache_rows
 #define HS_ATTN_STATUS_TIMEOUT 0x1u
 
 /* Synchronises the device, then returns in *status and clears the
- * HS_ATTN_STATUS_* bits that hs_sparse_attention calls have set on the
- * current device since the last call (0: none).  Errors:
+ * HS_ATTN_STATUS_* bits that hs_sparse_attention and hs_prefix_attention
+ * calls have set on the current device since the last call (0: none).  Errors:
  * HS_ERR_INVALID_ARG (status == NULL), HS_ERR_CUDA. */
 int hs_attention_status(uint32_t *status);
 
@@ -562,7 +562,9 @@ size_t hs_prefix_attention_bytes(int32_t n_req, int32_t q_heads, int32_t heads,
  * rounded once to bf16 for its product with the value, and the output once.
  * The work split depends on the arguments and the device only, so equal
  * inputs give bit-identical outputs.  Nothing is allocated; n_req == 0
- * enqueues nothing; n_req <= 65535, prefix_len < 2^31.
+ * enqueues nothing; n_req <= 65535, prefix_len < 2^31, k <= 2^30.  A
+ * pipeline wait that runs out of time (one second) makes the affected outputs
+ * NaN and sets HS_ATTN_STATUS_TIMEOUT (hs_attention_status).
  * Errors: HS_ERR_INVALID_ARG (also a workspace that is too small),
  * HS_ERR_CUDA.
  */

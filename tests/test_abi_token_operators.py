@@ -139,9 +139,10 @@ def test_workspace_sizes_are_zero_for_refused_arguments():
     assert hs.hs_attention_weights_bytes(0, 8, 8, 4) == 0
     assert hs.hs_attention_weights_bytes(1, 12, 8, 4) == 0
     assert hs.hs_attention_weights_bytes(1, 8, 8, 0) == 0
-    assert hs.hs_prefix_attention_bytes(1, 8, 8, 0, 4) == 0
+    assert hs.hs_prefix_attention_bytes(1, 8, 8, 0, 0) == 0
     assert hs.hs_prefix_attention_bytes(70000, 8, 8, 10, 4) == 0
     assert hs.hs_prefix_attention_bytes(1, 8, 8, 1 << 31, 4) == 0
+    assert hs.hs_prefix_attention_bytes(1, 8, 8, 100, (1 << 30) + 1) == 0
 
 
 def _select(lib, **kw):
