@@ -13,9 +13,15 @@
 // 2^64 -- one integer multiply -- is the angle's exact fraction of a turn;
 // its top 32 bits, as a signed fraction of half a turn, go to sincospif.
 //
-// Work split: eight lanes share a head, each with 16 bytes of either half of
-// it, so that a pair (i, i + 64) of a fully rotated head is in one lane and
-// the sum of squares takes three shuffles.  A warp reads four heads at a time.
+// Bound by HBM: every head is read once and written once.  Eight lanes share
+// a head, two 16-byte chunks of it each, chosen so that both ends of every
+// rotated pair are in one lane: the chunks of dimensions 8 l and
+// rot_dim / 2 + 8 l (the two halves of the rotated part), then what does not
+// rotate; or, interleaved, the lane's 16 consecutive dimensions.  The lane's
+// pairs are numbers 8 l to 8 l + 7 either way.  The sum of squares takes
+// three shuffles.  A warp takes one token and a run of its heads, four at a
+// time with the loads of sixteen in flight, and computes the token's angles
+// once, while the first of them arrive.
 #include <cstdint>
 
 #include "hs.h"
@@ -45,112 +51,166 @@ __device__ __forceinline__ uint4 pack8(const float *f) {
     return make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
 }
 
-// One octet of lanes per (token, head); heads in the order queries, keys,
-// values.  Element e of the lane: dimension 8 ol + e (e < 8) or
-// 64 + 8 ol + e - 8.
-__global__ void __launch_bounds__(kQkThreads) qk_norm_rope_kernel(const QkArgs a) {
-    const int ol = threadIdx.x & 7;
-    const int per_tok = a.q_heads + 2 * a.heads;
-    const int64_t total = (int64_t)a.n_tok * per_tok;
-    const int64_t step = (int64_t)gridDim.x * (kQkThreads / 8);
-    const int64_t first = (int64_t)blockIdx.x * (kQkThreads / 8) + threadIdx.x / 8;
-    // every octet of a warp goes round the loop the same number of times
-    // (shuffles below); those past the end work on nothing
-    const int64_t rounds = (total + step - 1) / step;
-    for (int64_t it = 0; it < rounds; ++it) {
-        const int64_t unit = first + it * step;
-        const bool live = unit < total;
-        const int64_t tok = live ? unit / per_tok : 0;
-        const int head = live ? (int)(unit - tok * per_tok) : 0;
-        int64_t row = 0;
-        if (head >= a.q_heads) row = a.rows ? a.rows[tok] : tok;
-        const bool store = live && (head < a.q_heads || (row >= 0 && row < a.record_rows));
-        const uint8_t *src;
-        uint8_t *dst;
-        if (head < a.q_heads) {
-            src = a.q + (tok * a.q_stride + (int64_t)head * kDim) * 2;
-            dst = a.q_out + (tok * a.q_heads + head) * (int64_t)(kDim * 2);
-        } else if (head < a.q_heads + a.heads) {
-            src = a.k + (tok * a.k_stride + (int64_t)(head - a.q_heads) * kDim) * 2;
-            dst = a.records + (row * 2 * a.heads + (head - a.q_heads)) * (int64_t)(kDim * 2);
-        } else {
-            src = a.v + (tok * a.v_stride + (int64_t)(head - a.q_heads - a.heads) * kDim) * 2;
-            dst = a.records + (row * 2 * a.heads + (head - a.q_heads)) * (int64_t)(kDim * 2);
-        }
-        uint4 x0 = make_uint4(0, 0, 0, 0), x1 = x0;
-        if (store) {
-            x0 = *reinterpret_cast<const uint4 *>(src + ol * 16);
-            x1 = *reinterpret_cast<const uint4 *>(src + 128 + ol * 16);
-        }
-        const bool value = head >= a.q_heads + a.heads;
-        float f[16];
-        unpack8(x0, f);
-        unpack8(x1, f + 8);
-        float ss = 0.f;
+constexpr int kBatch = 4;  // loads in flight: kBatch heads per octet
+
+__device__ __forceinline__ uint4 load16(const void *p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+
+// Unit = (token, run of `run` heads, a multiple of four, in the order queries,
+// keys, values); one warp each.
+template <bool kInterleaved>
+__global__ void __launch_bounds__(kQkThreads) qk_norm_rope_kernel(const QkArgs a, int run,
+                                                                  int runs) {
+    const int lane = threadIdx.x & 31, ol = lane & 7, oct = lane >> 3;
+    const int64_t unit = (int64_t)blockIdx.x * (kQkThreads / 32) + (threadIdx.x >> 5);
+    const int64_t tok = unit / runs;
+    if (tok >= a.n_tok) return;
+    const int h0 = (int)(unit - tok * runs) * run;
+    const int all = a.q_heads + 2 * a.heads;
+    const int h1 = min(all, h0 + run);
+    const bool turns = ol < a.rot_dim / 16;  // this lane's pairs rotate
+    // byte offsets of the lane's two chunks
+    int c0, c1;
+    if (kInterleaved) {
+        c0 = ol * 32;
+        c1 = c0 + 16;
+    } else if (turns) {
+        c0 = ol * 16;
+        c1 = c0 + a.rot_dim;                 // rot_dim / 2 elements further
+    } else {
+        c0 = a.rot_dim * 2 + (ol - a.rot_dim / 16) * 32;
+        c1 = c0 + 16;
+    }
+    // where head hd of the token is read and written (null: not written)
+    int64_t row = tok;
+    if (a.rows && h1 > a.q_heads) row = __ldg(a.rows + tok);
+    const bool keep = row >= 0 && row < a.record_rows;
+    auto source = [&](int hd) -> const uint8_t * {
+        if (hd < a.q_heads) return a.q + (tok * a.q_stride + (int64_t)hd * kDim) * 2;
+        hd -= a.q_heads;
+        if (hd < a.heads) return a.k + (tok * a.k_stride + (int64_t)hd * kDim) * 2;
+        return a.v + (tok * a.v_stride + (int64_t)(hd - a.heads) * kDim) * 2;
+    };
+    auto target = [&](int hd) -> uint8_t * {
+        if (hd < a.q_heads) return a.q_out + (tok * a.q_heads + hd) * (int64_t)(kDim * 2);
+        return keep ? a.records + (row * 2 * a.heads + (hd - a.q_heads)) * (int64_t)(kDim * 2)
+                    : nullptr;
+    };
+
+    uint4 x0[kBatch], x1[kBatch];
+    auto load = [&](int b0) {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) ss += f[e] * f[e];
-#pragma unroll
-        for (int d = 1; d < 8; d <<= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, d);
-        const float rs = rsqrtf(ss * (1.f / kDim) + a.eps);
-        const uint8_t *w = head < a.q_heads ? a.wq : a.wk;
-        if (w) {
-            float g[16];
-            unpack8(*reinterpret_cast<const uint4 *>(w + ol * 16), g);
-            unpack8(*reinterpret_cast<const uint4 *>(w + 128 + ol * 16), g + 8);
-#pragma unroll
-            for (int e = 0; e < 16; ++e) f[e] = f[e] * rs * g[e];
-        } else {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) f[e] *= rs;
-        }
-        const uint32_t pos = a.rot_dim && live ? (uint32_t)a.pos[tok] : 0u;
-        float y[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-            const int dim = (e < 8 ? 0 : 64) + 8 * ol + (e & 7);
-            // the dimension this one is paired with, its place, and the pair's number
-            int pd = dim, i = 0;
-            bool second = false;
-            if (dim < a.rot_dim) {
-                if (a.interleaved) {
-                    pd = dim ^ 1;
-                    i = dim >> 1;
-                    second = dim & 1;
-                } else {
-                    const int half = a.rot_dim / 2;
-                    second = dim >= half;
-                    pd = second ? dim - half : dim + half;
-                    i = second ? dim - half : dim;
-                }
-            }
-            // its value: element pe of lane (pd % 64) / 8 of the octet
-            const int pl = (pd & 63) >> 3, pe = (pd & 7) + (pd >= 64 ? 8 : 0);
-            float other = 0.f;
-            for (int c = 0; c < 16; ++c) {
-                const float v = __shfl_sync(0xFFFFFFFFu, f[c], pl, 8);
-                if (c == pe) other = v;
-            }
-            y[e] = f[e];
-            if (dim < a.rot_dim) {
-                const uint64_t turn = (uint64_t)(int64_t)(int32_t)pos * a.freq[i];
-                float sn, cs;
-                sincospif((float)(int32_t)(turn >> 32) * 0x1p-31f, &sn, &cs);
-                y[e] = second ? other * sn + f[e] * cs : f[e] * cs - other * sn;
+        for (int b = 0; b < kBatch; ++b) {
+            const int hd = b0 + b * 4 + oct;
+            x0[b] = x1[b] = make_uint4(0u, 0u, 0u, 0u);
+            if (hd < h1) {
+                const uint8_t *src = source(hd);
+                x0[b] = load16(src + c0);
+                x1[b] = load16(src + c1);
             }
         }
-        if (store) {
-            *reinterpret_cast<uint4 *>(dst + ol * 16) = value ? x0 : pack8(y);
-            *reinterpret_cast<uint4 *>(dst + 128 + ol * 16) = value ? x1 : pack8(y + 8);
+    };
+    load(h0);
+    float cs[8], sn[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        cs[e] = 1.f;
+        sn[e] = 0.f;
+    }
+    if (turns && h0 < a.q_heads + a.heads) {
+        const uint64_t pos = (uint64_t)(int64_t)__ldg(a.pos + tok);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const uint64_t turn = pos * a.freq[8 * ol + e];
+            sincospif((float)(int32_t)(turn >> 32) * 0x1p-31f, &sn[e], &cs[e]);
         }
     }
+    const uint4 one = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
+    uint4 wq0 = one, wq1 = one, wk0 = one, wk1 = one;
+    if (a.wq) {
+        wq0 = load16(a.wq + c0);
+        wq1 = load16(a.wq + c1);
+    }
+    if (a.wk) {
+        wk0 = load16(a.wk + c0);
+        wk1 = load16(a.wk + c1);
+    }
+
+    for (int b0 = h0; b0 < h1; b0 += kBatch * 4) {
+        if (b0 > h0) load(b0);
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            const int hd = b0 + b * 4 + oct;
+            if (b0 + b * 4 >= h1) break;     // the whole warp
+            uint4 y0 = x0[b], y1 = x1[b];
+            if (b0 + b * 4 < a.q_heads + a.heads) {  // some octet has a query or key
+                float f[16], g[16];
+                unpack8(y0, f);
+                unpack8(y1, f + 8);
+                float ss = 0.f;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) ss += f[e] * f[e];
+#pragma unroll
+                for (int d = 1; d < 8; d <<= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, d);
+                const float rs = rsqrtf(ss * (1.f / kDim) + a.eps);
+                const bool query = hd < a.q_heads;
+                unpack8(query ? wq0 : wk0, g);
+                unpack8(query ? wq1 : wk1, g + 8);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) f[e] = f[e] * rs * g[e];
+                if (turns) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        // pair e of the lane
+                        const int i = kInterleaved ? 2 * e : e, j = kInterleaved ? 2 * e + 1 : e + 8;
+                        const float u = f[i] * cs[e] - f[j] * sn[e];
+                        f[j] = f[i] * sn[e] + f[j] * cs[e];
+                        f[i] = u;
+                    }
+                }
+                if (hd < a.q_heads + a.heads) {
+                    y0 = pack8(f);
+                    y1 = pack8(f + 8);
+                }
+            }
+            if (hd < h1) {
+                uint8_t *dst = target(hd);
+                if (dst) {
+                    *reinterpret_cast<uint4 *>(dst + c0) = y0;
+                    *reinterpret_cast<uint4 *>(dst + c1) = y1;
+                }
+            }
+        }
+    }
+    // The records may be host memory that a resolve behind this launch starts
+    // reading before the grid's own flush: they are there before the CTA ends.
+    if (h1 > a.q_heads) __threadfence_system();
 }
 
 }  // namespace
 
+// Heads per warp: all of a token's where there are tokens enough for the SMs,
+// fewer (down to four) where there are not, so that a decode step's few
+// tokens still spread.
 cudaError_t launch_qk_norm_rope(const QkArgs &a, cudaStream_t st) {
-    const int64_t units = (int64_t)a.n_tok * (a.q_heads + 2 * a.heads);
-    const int64_t blocks = (units + kQkThreads / 8 - 1) / (kQkThreads / 8);
-    qk_norm_rope_kernel<<<(unsigned)(blocks < 152 * 8 ? blocks : 152 * 8), kQkThreads, 0, st>>>(a);
+    const int all = a.q_heads + 2 * a.heads;
+    const int quads = (all + 3) / 4;
+    int runs = 1;
+    while (runs < quads && (int64_t)a.n_tok * runs < kSms * 16) runs *= 2;
+    if (runs > quads) runs = quads;
+    const int run = (quads + runs - 1) / runs * 4;
+    runs = (all + run - 1) / run;
+    const int64_t units = (int64_t)a.n_tok * runs;
+    const unsigned blocks = (unsigned)((units + kQkThreads / 32 - 1) / (kQkThreads / 32));
+    if (a.interleaved)
+        qk_norm_rope_kernel<true><<<blocks, kQkThreads, 0, st>>>(a, run, runs);
+    else
+        qk_norm_rope_kernel<false><<<blocks, kQkThreads, 0, st>>>(a, run, runs);
     return cudaGetLastError();
 }
 
