@@ -1,21 +1,30 @@
 // The positions a request keeps by accumulated attention weight
 // (hs_select_heavy): the `recent` last ones and the heaviest of the others.
 //
-// A radix selection: a weight becomes a 32-bit key whose unsigned order is
-// the weights' order; three passes of 11, 11 and 10 bits count the keys that
-// share the prefix found so far and narrow down the key T of the last
-// position kept, then the positions with keys above T, and the first of
-// those equal to it, are written in ascending order.  The operator reads
-// every weight once and has few operations: the floor is the read, what it
-// spends is latency, one pass behind the other.
+// The operator reads every weight once and computes little: the floor is the
+// read, and what it spends beyond is latency, one step behind the other.
 //
 // A cluster of up to 16 CTAs takes a request, each a contiguous range of its
-// positions, read from global memory once and kept in shared memory as keys
-// (what does not fit is read again, from L2).  The counts of a pass are added
-// into CTA 0's through distributed shared memory, where one scan finds the
-// bin.  A weight of exactly 0 -- a position that was never selected -- is
-// often the most frequent, so its count is taken by ballot, as is that of the
-// first lane's bin: what is left for shared-memory atomics seldom collides.
+// positions, read once and kept in shared memory (what does not fit is read
+// again, from L2).  A weight's key is a 32-bit number whose unsigned order is
+// the weights' order.  T, the key of the last position kept, is found in three
+// steps:
+//   a bound B <= T: the maxima of groups of weights, one to four groups to a
+//     thread; at least as many groups as positions are wanted have a maximum
+//     at or above B, the lower edge of a bin of the maxima's leading 11 bits;
+//   the candidates: all keys above B, a little more than are wanted, listed
+//     with their positions.  If they are fewer, T = B (many equal weights:
+//     zeros, above all);
+//   T among the candidates, whose keys every CTA copies from all lists: counts
+//     in 2048 bins over their own range, and again within the bin found until
+//     it holds no more keys than a warp can rank.
+// So all weights are only compared with B, once; and the CTAs wait for one
+// another twice, once for the maxima's counts and once for the lists.  With
+// more candidates than the lists hold (a large k) every CTA counts all its
+// keys instead, by 11, 11 and 10 bits.
+// The kept positions -- keys above T, and the first of those equal to it --
+// are marked in two bitmaps over the CTA's range, whose prefix sums give each
+// its place in ascending order.
 #include <cmath>
 #include <cstdint>
 
@@ -33,9 +42,15 @@ constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kSelCluster = 16;
-constexpr int kKeysMax = 51200;       // keys a CTA keeps in shared memory
+constexpr int kListMax = 8192;        // candidates of the whole cluster
 constexpr int kMinChunk = 2048;       // positions per CTA worth splitting for
-constexpr int kUnroll = 8;            // loads in flight per thread
+// Weights and candidates that a CTA keeps in shared memory, candidates of a
+// CTA in a small cluster and in one of eight or more
+constexpr int kHeldMax = 36864, kHeldMaxWide = 49152;
+constexpr int kListWide = 2048;
+constexpr int kWindow = kBins * 32;   // positions the bitmaps hold
+static_assert((kHeldMax + 2 * kListMax) * 4 + 17408 <= 232448, "beside the static arrays");
+static_assert((kHeldMaxWide + 2 * kListWide) * 4 + 17408 <= 232448, "beside the static arrays");
 
 // Unsigned order of the keys = order of the weights; -0 counts as 0, NaN as
 // -infinity.
@@ -63,14 +78,49 @@ __device__ __forceinline__ void count(uint32_t *hist, uint32_t key, int shift, u
     }
 }
 
+// The bin, counted from the top, in which the need-th key lies: found[0] the
+// bin, found[1] how many of it are wanted, found[2] how many it holds;
+// unchanged if there are fewer keys.  One CTA, all threads; empties the counts.
+__device__ __forceinline__ void find_bin(uint32_t *counts, uint32_t need, uint32_t *warp_sum,
+                                         volatile uint32_t *found) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    // thread t has bins 2047 - 2t and 2046 - 2t
+    const int b = kBins - 1 - 2 * tid;
+    const uint32_t c0 = counts[b], c1 = counts[b - 1];
+    counts[b] = counts[b - 1] = 0;
+    uint32_t incl = c0 + c1;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+        if (lane >= d) incl += y;
+    }
+    if (lane == 31) warp_sum[warp] = incl;
+    __syncthreads();
+    uint32_t before = incl - c0 - c1;
+    before += __reduce_add_sync(0xFFFFFFFFu, lane < warp ? warp_sum[lane] : 0u);
+    if (before < need && need <= before + c0 + c1) {
+        const bool second = need > before + c0;
+        found[0] = (uint32_t)(second ? b - 1 : b);
+        found[1] = need - before - (second ? c0 : 0u);
+        found[2] = second ? c1 : c0;
+    }
+}
+
 __global__ void __launch_bounds__(kSelThreads)
-    select_heavy_kernel(const SelectArgs a, int ctas) {
-    extern __shared__ uint32_t keys[];
-    __shared__ uint32_t hist[kBins];   // this CTA's counts
-    __shared__ uint32_t sums[kBins];   // CTA 0: the cluster's
-    __shared__ uint32_t warp_a[kSelWarps], warp_b[kSelWarps];
-    __shared__ uint32_t found[2];      // CTA 0: the bin, and how many of it are wanted
-    __shared__ uint32_t totals[2][kSelCluster];
+    select_heavy_kernel(const SelectArgs a, int ctas, int held_max, int list_max) {
+    // the weights held, later all candidates' keys [max(held_max, kListMax)];
+    // this CTA's candidates: keys, positions [list_max] each
+    extern __shared__ __align__(16) uint32_t dyn[];
+    float *vals = reinterpret_cast<float *>(dyn);
+    uint32_t *all = dyn;
+    uint32_t *list = dyn + max(held_max, kListMax);
+    int32_t *list_pos = reinterpret_cast<int32_t *>(list + list_max);
+    // this CTA's counts and the cluster's, zero between uses; in the end the
+    // bitmaps of the keys above T and equal to it
+    __shared__ uint32_t hist[kBins], sums[kBins];
+    __shared__ uint32_t warp_a[kSelWarps], warp_b[kSelWarps], few[32], ahead_b[kSelWarps];
+    __shared__ uint32_t found[3], highest, n_few, n_list;
+    __shared__ uint32_t totals[2][kSelCluster], list_counts[kSelCluster];
     cg::cluster_group cluster = cg::this_cluster();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int i = blockIdx.x / ctas, rank = blockIdx.x % ctas;
@@ -85,7 +135,7 @@ __global__ void __launch_bounds__(kSelThreads)
     len = len < 0 ? 0 : len > a.n_positions ? a.n_positions : len;
     const int recent = (int)(len < a.recent ? len : a.recent);
     const int64_t n = len - recent;         // positions that compete
-    const int want = (int)(n < a.k - recent ? n : a.k - recent);
+    const uint32_t want = (uint32_t)(n < a.k - recent ? n : a.k - recent);
     // the ends that need no selection
     for (int j = rank * kSelThreads + tid; j < recent; j += ctas * kSelThreads)
         out[want + j] = (int32_t)(n + j);
@@ -96,143 +146,387 @@ __global__ void __launch_bounds__(kSelThreads)
     const int64_t chunk = (n + ctas - 1) / ctas;
     const int64_t lo = min(n, rank * chunk);
     const int size = (int)(min(n, lo + chunk) - lo);  // this CTA's positions
-    const int held = min(size, kKeysMax);
     const float *wc = w + lo;
-    for (int b = tid; b < kBins; b += kSelThreads) hist[b] = sums[b] = 0;
-    __syncthreads();
-    cluster.barrier_arrive();               // CTA 0's sums are zero
-
-    uint32_t prefix = 0, need = (uint32_t)want;
-    for (int pass = 0; pass < 3; ++pass) {
-        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-        const uint32_t mask = pass == 2 ? 1023u : 2047u;
-        const int above = shift + (pass == 2 ? 10 : 11);
-        if (pass == 0) {
-            for (int j0 = 0; j0 < size; j0 += kUnroll * kSelThreads) {
-                float x[kUnroll];
+    // vector v holds positions 4 v - off .. 4 v - off + 3 of the range, so that
+    // whole vectors are aligned in global memory; -infinity outside the range
+    const int off = (int)(reinterpret_cast<uintptr_t>(wc) >> 2 & 3);
+    const int nv = (off + size + 3) / 4;
+    const int held = min(nv, held_max / 4);
+    // Vectors v, v + 1024, ..., kEach of them: those below `from` out of shared
+    // memory, the others with their global loads issued together.
+    constexpr int kEach = 4;
+    auto at = [&](int v, int from, float4 *x) {
 #pragma unroll
-                for (int u = 0; u < kUnroll; ++u) {
-                    const int j = j0 + u * kSelThreads + tid;
-                    x[u] = j < size ? __ldg(wc + j) : 0.f;
-                }
-#pragma unroll
-                for (int u = 0; u < kUnroll; ++u) {
-                    const int j = j0 + u * kSelThreads + tid;
-                    if (j0 + u * kSelThreads >= size) break;
-                    const uint32_t key = order_key(x[u]);
-                    if (j < held) keys[j] = key;
-                    count(hist, key, shift, mask, j < size, lane);
-                }
-            }
-        } else {
-            for (int j0 = 0; j0 < size; j0 += kSelThreads) {
-                const int j = j0 + tid;
-                const uint32_t key = j < held ? keys[j] : j < size ? order_key(__ldg(wc + j)) : 0u;
-                count(hist, key, shift, mask, j < size && key >> above == prefix, lane);
+        for (int u = 0; u < kEach; ++u) {
+            const int t = v + u * kSelThreads, j = 4 * t - off;
+            if (t < from) {
+                x[u] = reinterpret_cast<const float4 *>(vals)[t];
+            } else if (j >= 0 && j + 3 < size) {
+                x[u] = __ldg(reinterpret_cast<const float4 *>(wc + j));
+            } else {
+                x[u] = make_float4(j >= 0 && j < size ? __ldg(wc + j) : -INFINITY,
+                                   j + 1 >= 0 && j + 1 < size ? __ldg(wc + j + 1) : -INFINITY,
+                                   j + 2 >= 0 && j + 2 < size ? __ldg(wc + j + 2) : -INFINITY,
+                                   j + 3 >= 0 && j + 3 < size ? __ldg(wc + j + 3) : -INFINITY);
             }
         }
-        __syncthreads();
-        if (pass == 0) cluster.barrier_wait();
-        uint32_t *lead = cluster.map_shared_rank(sums, 0);
+    };
+    // Calls f(key, position, whether it is one) for every element of the vectors
+    auto each = [&](int v, const float4 *x, auto f) {
+#pragma unroll
+        for (int u = 0; u < kEach; ++u) {
+            const int j = 4 * (v + u * kSelThreads) - off;
+            f(order_key(x[u].x), j, j >= 0 && j < size);
+            f(order_key(x[u].y), j + 1, j + 1 >= 0 && j + 1 < size);
+            f(order_key(x[u].z), j + 2, j + 2 >= 0 && j + 2 < size);
+            f(order_key(x[u].w), j + 3, j + 3 >= 0 && j + 3 < size);
+        }
+    };
+
+    // ---- read; the maxima's leading bits ------------------------------------
+    for (int b = tid; b < kBins; b += kSelThreads) hist[b] = sums[b] = 0;
+    if (tid == 0) found[0] = highest = n_list = 0;
+    float4 top = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+    for (int v0 = 0; v0 < nv; v0 += kEach * kSelThreads) {
+        float4 x[kEach];
+        at(v0 + tid, 0, x);
+#pragma unroll
+        for (int u = 0; u < kEach; ++u) {
+            const int v = v0 + u * kSelThreads + tid;
+            if (v < held) reinterpret_cast<float4 *>(vals)[v] = x[u];
+            top.x = fmaxf(top.x, x[u].x);   // of a number and NaN, the number
+            top.y = fmaxf(top.y, x[u].y);
+            top.z = fmaxf(top.z, x[u].z);
+            top.w = fmaxf(top.w, x[u].w);
+        }
+    }
+    __syncthreads();
+    cluster.barrier_arrive();               // this CTA's sums are zero
+    // as few groups as are half as many again as the positions wanted
+    const uint32_t groups = (uint32_t)ctas * kSelThreads;
+    if (2 * groups >= 3 * want) {
+        count(hist, order_key(fmaxf(fmaxf(top.x, top.y), fmaxf(top.z, top.w))), 21, 2047u, true,
+              lane);
+    } else if (4 * groups >= 3 * want) {
+        count(hist, order_key(fmaxf(top.x, top.y)), 21, 2047u, true, lane);
+        count(hist, order_key(fmaxf(top.z, top.w)), 21, 2047u, true, lane);
+    } else {
+        count(hist, order_key(top.x), 21, 2047u, true, lane);
+        count(hist, order_key(top.y), 21, 2047u, true, lane);
+        count(hist, order_key(top.z), 21, 2047u, true, lane);
+        count(hist, order_key(top.w), 21, 2047u, true, lane);
+    }
+    __syncthreads();
+    cluster.barrier_wait();
+    // adds this CTA's counts to every CTA's sums
+    auto add_counts = [&]() {
         for (int b = tid; b < kBins; b += kSelThreads) {
-            if (hist[b]) atomicAdd(&lead[b], hist[b]);
+            const uint32_t c = hist[b];
+            if (c)
+                for (int t = 0; t < ctas; ++t) atomicAdd(cluster.map_shared_rank(sums, t) + b, c);
             hist[b] = 0;
         }
-        cluster.sync();
-        if (rank == 0) {
-            // thread t has bins 2047 - 2t and 2046 - 2t; how many keys lie above
-            const int b = kBins - 1 - 2 * tid;
-            const uint32_t c0 = sums[b], c1 = sums[b - 1];
-            sums[b] = sums[b - 1] = 0;
-            uint32_t incl = c0 + c1;
+    };
+    add_counts();
+    cluster.sync();
+    find_bin(sums, want, warp_a, found);
+    __syncthreads();
+    const uint32_t B = found[0] << 21;
+
+    // ---- the candidates: keys above B ----------------------------------------
+    auto list_one = [&](uint32_t key, int j) {
+        const uint32_t e = atomicAdd(&n_list, 1u);
+        if (e < (uint32_t)list_max) {
+            list[e] = key;
+            list_pos[e] = j;
+        }
+    };
+    if (B >= 0x00800000u) {                 // above -infinity: compared as numbers
+        const float fb = __uint_as_float(B & 0x80000000u ? B ^ 0x80000000u : ~B);
+        for (int v0 = 0; v0 < nv; v0 += kEach * kSelThreads) {
+            float4 x[kEach];
+            at(v0 + tid, held, x);
 #pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, incl, d);
-                if (lane >= d) incl += y;
-            }
-            if (lane == 31) warp_a[warp] = incl;
-            __syncthreads();
-            uint32_t before = incl - c0 - c1;
-            for (int v = 0; v < warp; ++v) before += warp_a[v];
-            if (before < need && need <= before + c0 + c1) {
-                const bool second = need > before + c0;
-                found[0] = (uint32_t)(second ? b - 1 : b);
-                found[1] = need - before - (second ? c0 : 0u);
+            for (int u = 0; u < kEach; ++u) {
+                if (!(fmaxf(fmaxf(x[u].x, x[u].y), fmaxf(x[u].z, x[u].w)) > fb)) continue;
+                const int j = 4 * (v0 + u * kSelThreads + tid) - off;
+                if (x[u].x > fb) list_one(order_key(x[u].x), j);
+                if (x[u].y > fb) list_one(order_key(x[u].y), j + 1);
+                if (x[u].z > fb) list_one(order_key(x[u].z), j + 2);
+                if (x[u].w > fb) list_one(order_key(x[u].w), j + 3);
             }
         }
-        cluster.sync();
-        const uint32_t *f = cluster.map_shared_rank(found, 0);
-        prefix = prefix << (pass == 2 ? 10 : 11) | f[0];
-        need = f[1];
-    }
-
-    // keys above T are kept, and the first `need` positions of those equal to
-    // it.  Each warp walks a contiguous part, twice: to count, and to write.
-    const uint32_t T = prefix;
-    const int part = (int)((chunk + kSelThreads - 1) / kSelThreads) * 32;
-    const int p0 = min(size, warp * part), p1 = min(size, p0 + part);
-    auto key_at = [&](int j) {
-        return j < held ? keys[j] : order_key(__ldg(wc + j));
-    };
-    uint32_t n_gt = 0, n_eq = 0;
-    for (int j = p0 + lane; j < p1; j += 32) {
-        const uint32_t key = key_at(j);
-        n_gt += key > T;
-        n_eq += key == T;
-    }
-    n_gt = __reduce_add_sync(0xFFFFFFFFu, n_gt);
-    n_eq = __reduce_add_sync(0xFFFFFFFFu, n_eq);
-    if (lane == 0) {
-        warp_a[warp] = n_gt;
-        warp_b[warp] = n_eq;
+    } else {
+        for (int v0 = 0; v0 < nv; v0 += kEach * kSelThreads) {
+            float4 x[kEach];
+            at(v0 + tid, held, x);
+            each(v0 + tid, x, [&](uint32_t key, int j, bool is) {
+                if (is && key > B) list_one(key, j);
+            });
+        }
     }
     __syncthreads();
-    uint32_t gt0 = 0, eq0 = 0, gt_all = 0, eq_all = 0;
-    {
-        const uint32_t ga = warp_a[lane], eb = warp_b[lane];
-        gt0 = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? ga : 0u);
-        eq0 = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? eb : 0u);
-        gt_all = __reduce_add_sync(0xFFFFFFFFu, ga);
-        eq_all = __reduce_add_sync(0xFFFFFFFFu, eb);
+    if (tid < ctas) cluster.map_shared_rank(list_counts, tid)[rank] = n_list;
+    cluster.sync();
+    uint64_t candidates = 0;
+    bool listed = true;                     // the lists hold all candidates
+    for (int c = 0; c < ctas; ++c) {
+        candidates += list_counts[c];
+        listed &= list_counts[c] <= (uint32_t)list_max;
     }
-    if (tid < ctas) {
-        cluster.map_shared_rank(totals[0], tid)[rank] = gt_all;
-        cluster.map_shared_rank(totals[1], tid)[rank] = eq_all;
-    }
-    cluster.sync();  // also the last access to another CTA's shared memory
-    for (int c = 0; c < rank; ++c) {
-        gt0 += totals[0][c];
-        eq0 += totals[1][c];
-    }
-    const uint32_t below = (1u << lane) - 1u;
-    for (int j0 = p0; j0 < p1; j0 += 32) {
-        const int j = j0 + lane;
-        const uint32_t key = j < p1 ? key_at(j) : 0u;
-        const uint32_t gt = __ballot_sync(0xFFFFFFFFu, j < p1 && key > T);
-        const uint32_t eq = __ballot_sync(0xFFFFFFFFu, j < p1 && key == T);
-        if (gt | eq) {
-            const uint32_t e = eq0 + __popc(eq & below);
-            if ((gt >> lane & 1u) || ((eq >> lane & 1u) && e < need))
-                out[gt0 + __popc(gt & below) + min(e, need)] = (int32_t)(lo + j);
-            gt0 += __popc(gt);
-            eq0 += __popc(eq);
+    listed &= candidates <= kListMax;
+    const bool from_list = candidates >= want && listed;
+
+    uint32_t T = B, need = want - (uint32_t)candidates;
+    uint32_t gt0 = 0, eq0 = 0;              // kept and equal ones before this CTA's
+    if (from_list) {
+        // every CTA's candidates, in the order of the ranges: warps share the
+        // lists out
+        const int total = (int)candidates;
+        int before = 0;                     // candidates of lower ranges
+        {
+            const int per = kSelWarps / ctas, c = warp / per;
+            if (c < ctas) {
+                int start = 0;
+                for (int t = 0; t < c; ++t) start += (int)list_counts[t];
+                const uint32_t *src = cluster.map_shared_rank(list, c);
+                uint32_t most = 0;
+                for (int j = (warp - c * per) * 32 + lane; j < (int)list_counts[c]; j += per * 32) {
+                    const uint32_t key = src[j];
+                    all[start + j] = key;
+                    most = max(most, key);
+                }
+                most = __reduce_max_sync(0xFFFFFFFFu, most);
+                if (lane == 0) atomicMax(&highest, most);
+            }
+            for (int t = 0; t < rank; ++t) before += (int)list_counts[t];
+        }
+        __syncthreads();
+        cluster.barrier_arrive();           // the other CTAs' lists are read
+        // the need-th largest lies in [base, base + 2048 << shift)
+        uint32_t base = B;
+        need = want;
+        int shift = max(0, 32 - __clz(highest - B) - 11);
+        while (true) {
+            for (int j0 = 0; j0 < total; j0 += kSelThreads) {
+                const uint32_t x = j0 + tid < total ? all[j0 + tid] : 0u;
+                const uint32_t bin = (x - base) >> shift;
+                const bool in = j0 + tid < total && x >= base && bin < kBins;
+                const uint32_t some = __ballot_sync(0xFFFFFFFFu, in);
+                if (!some) continue;
+                // many equal keys: the first lane's bin in one addition
+                const int f = __ffs(some) - 1;
+                const uint32_t b0 = __shfl_sync(0xFFFFFFFFu, bin, f);
+                const uint32_t same = __ballot_sync(0xFFFFFFFFu, in && bin == b0);
+                if (lane == f) atomicAdd(&hist[b0], (uint32_t)__popc(same));
+                if (in && bin != b0) atomicAdd(&hist[bin], 1u);
+            }
+            if (tid == 0) n_few = 0;
+            __syncthreads();
+            find_bin(hist, need, warp_a, found);
+            __syncthreads();
+            base += found[0] << shift;
+            need = found[1];
+            if (shift == 0 || found[2] <= 32) break;
+            shift = max(0, shift - 11);
+            __syncthreads();                // every thread has read what was found
+        }
+        if (shift > 0) {
+            // at most 32 keys in the bin: every warp ranks them
+            for (int j = tid; j < total; j += kSelThreads) {
+                const uint32_t x = all[j];
+                if (x >= base && (x - base) >> shift == 0) few[atomicAdd(&n_few, 1u)] = x;
+            }
+            __syncthreads();
+            const uint32_t mine = lane < (int)n_few ? few[lane] : 0u;
+            uint32_t above = 0, ahead = 0;
+            for (int s = 0; s < 32; ++s) {
+                const uint32_t y = __shfl_sync(0xFFFFFFFFu, mine, s);
+                above += y > mine;
+                ahead += y == mine && s < lane;
+            }
+            const int src = __ffs(__ballot_sync(0xFFFFFFFFu, above + ahead + 1 == need)) - 1;
+            T = __shfl_sync(0xFFFFFFFFu, mine, src);
+            need -= __shfl_sync(0xFFFFFFFFu, above, src);
+        } else {
+            T = base;
+        }
+        for (int j = tid; j < before; j += kSelThreads) {
+            gt0 += all[j] > T;
+            eq0 += all[j] == T;
+        }
+    } else {
+        if (candidates >= want) {
+            uint32_t prefix = 0;
+            need = want;
+            for (int pass = 0; pass < 3; ++pass) {
+                const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+                const int bits = pass == 2 ? 10 : 11;
+                for (int v0 = 0; v0 < nv; v0 += kEach * kSelThreads) {
+                    float4 x[kEach];
+                    at(v0 + tid, held, x);
+                    each(v0 + tid, x, [&](uint32_t key, int, bool is) {
+                        count(hist, key, shift, (1u << bits) - 1u,
+                              is && (pass == 0 || key >> (shift + bits) == prefix), lane);
+                    });
+                }
+                __syncthreads();
+                add_counts();
+                cluster.sync();
+                find_bin(sums, need, warp_a, found);
+                cluster.sync();             // every CTA's sums are zero again
+                prefix = prefix << bits | found[0];
+                need = found[1];
+            }
+            T = prefix;
+        }
+        // kept and equal ones of every CTA
+        uint32_t n_gt = 0, n_eq = 0;
+        for (int v0 = 0; v0 < nv; v0 += kEach * kSelThreads) {
+            float4 x[kEach];
+            at(v0 + tid, held, x);
+            each(v0 + tid, x, [&](uint32_t key, int, bool is) {
+                n_gt += is && key > T;
+                n_eq += is && key == T;
+            });
+        }
+        if (tid < 2) totals[tid][rank] = 0;
+        __syncthreads();
+        n_gt = __reduce_add_sync(0xFFFFFFFFu, n_gt);
+        n_eq = __reduce_add_sync(0xFFFFFFFFu, n_eq);
+        if (lane == 0) {
+            atomicAdd(&totals[0][rank], n_gt);
+            atomicAdd(&totals[1][rank], n_eq);
+        }
+        __syncthreads();
+        if (tid < ctas && tid != rank) {
+            cluster.map_shared_rank(totals[0], tid)[rank] = totals[0][rank];
+            cluster.map_shared_rank(totals[1], tid)[rank] = totals[1][rank];
+        }
+        cluster.sync();
+        cluster.barrier_arrive();           // no other CTA's memory is needed
+        if (tid < rank) {
+            gt0 = totals[0][tid];
+            eq0 = totals[1][tid];
         }
     }
+    // (the sums over the threads are taken with the first window's)
+
+    // ---- marked and written in order -----------------------------------------
+    uint32_t *gt_bits = hist, *eq_bits = sums;
+    const int n_mine = from_list ? (int)list_counts[rank] : 0;
+    for (int w0 = 0; w0 < size || w0 == 0; w0 += kWindow) {
+        const int w1 = min(size - w0, kWindow);  // positions w0 + [0, w1)
+        auto mark = [&](uint32_t key, int j) {
+            if (key < T || j < 0 || j >= w1) return;
+            atomicOr((key > T ? gt_bits : eq_bits) + (j >> 5), 1u << (j & 31));
+        };
+        if (from_list) {
+            for (int j = tid; j < n_mine; j += kSelThreads) mark(list[j], list_pos[j] - w0);
+        } else {
+            // the vectors that reach into the window
+            for (int v0 = (w0 + off) / 4; 4 * v0 - off < w0 + w1; v0 += kEach * kSelThreads) {
+                float4 x[kEach];
+                at(v0 + tid, held, x);
+                each(v0 + tid, x, [&](uint32_t key, int j, bool is) {
+                    if (is) mark(key, j - w0);
+                });
+            }
+        }
+        const uint32_t g0 = __reduce_add_sync(0xFFFFFFFFu, gt0);
+        const uint32_t q0 = __reduce_add_sync(0xFFFFFFFFu, eq0);
+        __syncthreads();
+        // a thread writes one or two consecutive words
+        const int words = (w1 + 31) / 32, each_words = words > kSelThreads ? 2 : 1;
+        uint32_t g[2] = {0u, 0u}, q[2] = {0u, 0u};
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int b = each_words * tid + e;
+            if (e < each_words && b < words) {
+                g[e] = gt_bits[b];
+                q[e] = eq_bits[b];
+                gt_bits[b] = eq_bits[b] = 0;
+            }
+        }
+        const uint32_t ng = __popc(g[0]) + __popc(g[1]), nq = __popc(q[0]) + __popc(q[1]);
+        uint32_t ig = ng, iq = nq;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const uint32_t yg = __shfl_up_sync(0xFFFFFFFFu, ig, d);
+            const uint32_t yq = __shfl_up_sync(0xFFFFFFFFu, iq, d);
+            if (lane >= d) {
+                ig += yg;
+                iq += yq;
+            }
+        }
+        // a warp's words, and what its threads had before the window
+        if (lane == 31) {
+            warp_a[warp] = ig;
+            warp_b[warp] = iq;
+        }
+        if (lane == 0) {
+            few[warp] = g0;
+            ahead_b[warp] = q0;
+        }
+        __syncthreads();
+        const uint32_t wg = warp_a[lane], wq = warp_b[lane];
+        gt0 = __reduce_add_sync(0xFFFFFFFFu, few[lane]);
+        eq0 = __reduce_add_sync(0xFFFFFFFFu, ahead_b[lane]);
+        uint32_t pg = gt0 + ig - ng + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? wg : 0u);
+        uint32_t pq = eq0 + iq - nq + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? wq : 0u);
+        // carried on by one thread
+        const uint32_t next_g = gt0 + __reduce_add_sync(0xFFFFFFFFu, wg);
+        const uint32_t next_q = eq0 + __reduce_add_sync(0xFFFFFFFFu, wq);
+        gt0 = tid == 0 ? next_g : 0u;
+        eq0 = tid == 0 ? next_q : 0u;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            uint32_t any = g[e] | q[e];
+            while (any) {
+                const int b = __ffs(any) - 1;
+                any &= any - 1;
+                const bool above = g[e] >> b & 1u;
+                if (above || pq < need)
+                    out[pg + min(pq, need)] =
+                        (int32_t)(lo + w0 + (each_words * tid + e) * 32 + b);
+                pg += above;
+                pq += !above;
+            }
+        }
+        __syncthreads();                    // the window's words and sums are read
+    }
+    cluster.barrier_wait();
 }
 
 }  // namespace
 
-// The cluster of a request: as many CTAs, a power of two up to 16, as keep
-// the grid on the SMs at once and each at kMinChunk positions or more.
+// The cluster of a request: as many CTAs as have kMinChunk positions or more
+// each and as keep every request's cluster on the GPU at once with a CTA to an
+// SM -- a cluster lies within one GPC, whose SMs its size has to divide well
+// (cudaOccupancyMaxActiveClusters on GB300: 7 clusters of 16, 8 of 12, 15 of
+// 8, 36 of 4, 76 of 2; eight requests of 2^20 positions as clusters of 16 ran
+// in two waves, 47 us against 20 for one).
 cudaError_t launch_select_heavy(const SelectArgs &a, int n_req, cudaStream_t st) {
+    static const struct {
+        int ctas, clusters;
+    } sizes[] = {{16, 7}, {12, 8}, {8, 15}, {4, 36}, {2, 76}};
     int ctas = 1;
-    while (ctas < kSelCluster && (int64_t)n_req * 2 * ctas <= kSms &&
-           a.n_positions >= (int64_t)2 * ctas * kMinChunk)
-        ctas *= 2;
-    const int64_t chunk = (a.n_positions + ctas - 1) / ctas;
-    const size_t smem = (size_t)(chunk < kKeysMax ? chunk : kKeysMax) * 4;
+    for (const auto &s : sizes)
+        if (n_req <= s.clusters && a.n_positions >= (int64_t)s.ctas * kMinChunk) {
+            ctas = s.ctas;
+            break;
+        }
+    // a range's positions fit 31 bits with room for a step of the loops
+    while (a.n_positions > (int64_t)ctas << 30) ctas *= 2;
+    // a range's weights start at any of the four words of a vector
+    const bool wide = ctas >= 8;
+    const int most = wide ? kHeldMaxWide : kHeldMax, list_max = wide ? kListWide : kListMax;
+    const int64_t chunk = (a.n_positions + ctas - 1) / ctas + 3;
+    const int held_max = (int)(chunk < most ? (chunk + 3) / 4 * 4 : most);
+    const size_t smem = ((size_t)(held_max > kListMax ? held_max : kListMax) + 2 * list_max) * 4;
     cudaError_t e = cudaFuncSetAttribute(select_heavy_kernel,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kKeysMax * 4);
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         232448 - 17408);
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(select_heavy_kernel,
                                  cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
@@ -249,7 +543,7 @@ cudaError_t launch_select_heavy(const SelectArgs &a, int n_req, cudaStream_t st)
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, select_heavy_kernel, a, ctas);
+    return cudaLaunchKernelEx(&cfg, select_heavy_kernel, a, ctas, held_max, list_max);
 }
 
 }  // namespace hs
