@@ -329,43 +329,83 @@ __device__ __forceinline__ int64_t part_row(const GroupArgs &a, const Parts &x, 
                           : (x.rows_first + i - x.n_prefix) * a.q_heads + hq;
 }
 
+// M = max of the parts' maxima and L = sum 2^(m - M) l of (request, query
+// head), by one warp; the same in every lane.
+__device__ __forceinline__ float2 join(const GroupArgs &a, const RowsPlan &p, const PrefixPlan &pp,
+                                       const Parts &x, int r, int hq, int lane) {
+    float M = -INFINITY, L = 0.f;
+    bool bad = false;
+    for (int i = lane; i < x.n; i += 32) {
+        const float2 ml = (i < x.n_prefix ? pp.ml : p.ml)[part_row(a, x, i, r, hq)];
+        const float big = fmaxf(M, ml.x), base = big == -INFINITY ? 0.f : big;
+        L = L * exp2f(M - base) + ml.y * exp2f(ml.x - base);
+        M = big;
+        bad |= ml.x != ml.x;               // a part that a wait gave up on
+    }
+#pragma unroll
+    for (int d = 16; d; d >>= 1) {
+        const float m2 = __shfl_xor_sync(0xFFFFFFFFu, M, d);
+        const float l2 = __shfl_xor_sync(0xFFFFFFFFu, L, d);
+        const float big = fmaxf(M, m2), base = big == -INFINITY ? 0.f : big;
+        L = L * exp2f(M - base) + l2 * exp2f(m2 - base);
+        M = big;
+    }
+    if (__any_sync(0xFFFFFFFFu, bad)) M = __int_as_float(0x7FC00000);
+    return make_float2(M == -INFINITY ? 0.f : M, L);
+}
+
+// The first out_blocks CTAs write outputs, `share` warps to a (request, query
+// head), four dimensions per lane; the others the weights of 256 rows each.
 __global__ void __launch_bounds__(kMergeThreads)
-    merge_kernel(const GroupArgs a, const RowsPlan p, const PrefixPlan pp, int out_blocks) {
+    merge_kernel(const GroupArgs a, const RowsPlan p, const PrefixPlan pp, int out_blocks,
+                 int share) {
+    __shared__ float4 sum[kMergeThreads];
+    __shared__ float2 mi[128];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if ((int)blockIdx.x < out_blocks) {
-        // one warp per (request, query head), four dimensions per lane
-        const int64_t unit = (int64_t)blockIdx.x * (kMergeThreads / 32) + warp;
-        if (unit >= (int64_t)a.n_req * a.q_heads) return;
-        const int r = (int)(unit / a.q_heads), hq = (int)(unit % a.q_heads);
-        const Parts x = parts_of(p, pp.splits, r);
-        float M = -INFINITY;
-        bool bad = false;
-        for (int i = lane; i < x.n; i += 32) {
-            const float2 ml = (i < x.n_prefix ? pp.ml : p.ml)[part_row(a, x, i, r, hq)];
-            M = fmaxf(M, ml.x);
-            bad |= ml.x != ml.x;
-        }
-#pragma unroll
-        for (int d = 16; d; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, d));
-        if (__any_sync(0xFFFFFFFFu, bad)) M = __int_as_float(0x7FC00000);
-        const float base = M == -INFINITY ? 0.f : M;
-        float L = 0.f;
+        const int turn = warp % share;
+        const int64_t unit = ((int64_t)blockIdx.x * (kMergeThreads / 32) + warp) / share;
+        const bool live = unit < (int64_t)a.n_req * a.q_heads;
+        const int r = live ? (int)(unit / a.q_heads) : 0, hq = live ? (int)(unit % a.q_heads) : 0;
+        Parts x = parts_of(p, pp.splits, r);
+        if (!live) x.n = 0;
+        const float2 ML = join(a, p, pp, x, r, hq, lane);
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int i = 0; i < x.n; ++i) {
-            const int64_t row = part_row(a, x, i, r, hq);
-            const float2 ml = (i < x.n_prefix ? pp.ml : p.ml)[row];
-            const float4 v = *reinterpret_cast<const float4 *>(
-                (i < x.n_prefix ? pp.o : p.o) + row * kDim + lane * 4);
-            const float w = exp2f(ml.x - base);
-            L += w * ml.y;
-            acc.x += w * v.x;
-            acc.y += w * v.y;
-            acc.z += w * v.z;
-            acc.w += w * v.w;
+        constexpr int kLoads = 4;
+        for (int i0 = turn; i0 < x.n; i0 += kLoads * share) {
+            float4 v[kLoads];
+            float m[kLoads];
+#pragma unroll
+            for (int u = 0; u < kLoads; ++u) {
+                const int i = i0 + u * share;
+                if (i >= x.n) continue;
+                const int64_t row = part_row(a, x, i, r, hq);
+                v[u] = *reinterpret_cast<const float4 *>((i < x.n_prefix ? pp.o : p.o) +
+                                                         row * kDim + lane * 4);
+                m[u] = (i < x.n_prefix ? pp.ml : p.ml)[row].x;
+            }
+#pragma unroll
+            for (int u = 0; u < kLoads; ++u) {
+                if (i0 + u * share >= x.n) continue;
+                const float w = exp2f(m[u] - ML.x);
+                acc.x += w * v[u].x;
+                acc.y += w * v[u].y;
+                acc.z += w * v[u].z;
+                acc.w += w * v[u].w;
+            }
         }
-        const float inv = L == 0.f ? 0.f : 1.f / L;  // no row at all: zeros
+        sum[threadIdx.x] = acc;
+        __syncthreads();
+        if (turn != 0 || !live) return;
+        for (int s = 1; s < share; ++s) {
+            const float4 v = sum[threadIdx.x + s * 32];
+            acc.x += v.x;
+            acc.y += v.y;
+            acc.z += v.z;
+            acc.w += v.w;
+        }
+        const float inv = ML.y == 0.f ? 0.f : 1.f / ML.y;  // no row at all: zeros
         uint2 v;
         asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(v.x) : "f"(acc.y * inv), "f"(acc.x * inv));
         asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(v.y) : "f"(acc.w * inv), "f"(acc.z * inv));
@@ -373,31 +413,14 @@ __global__ void __launch_bounds__(kMergeThreads)
         return;
     }
     // weights: 256 rows of one request; its maximum and sum per query head first
-    __shared__ float2 mi[128];
     const int64_t chunk = (int64_t)blockIdx.x - out_blocks;
     const int per_req = (a.k + kMergeThreads - 1) / kMergeThreads;
     const int r = (int)(chunk / per_req);
     const int j = (int)(chunk % per_req) * kMergeThreads + threadIdx.x;
     const Parts x = parts_of(p, 0, r);
     for (int hq = warp; hq < a.q_heads; hq += kMergeThreads / 32) {
-        float M = -INFINITY, L = 0.f;
-        for (int i = lane; i < x.n; i += 32) {
-            const float2 ml = p.ml[part_row(a, x, i, r, hq)];
-            const float big = fmaxf(M, ml.x);
-            const float base = big == -INFINITY ? 0.f : big;
-            L = L * exp2f(M - base) + ml.y * exp2f(ml.x - base);
-            M = big;
-        }
-#pragma unroll
-        for (int d = 16; d; d >>= 1) {
-            const float m2 = __shfl_xor_sync(0xFFFFFFFFu, M, d);
-            const float l2 = __shfl_xor_sync(0xFFFFFFFFu, L, d);
-            const float big = fmaxf(M, m2);
-            const float base = big == -INFINITY ? 0.f : big;
-            L = L * exp2f(M - base) + l2 * exp2f(m2 - base);
-            M = big;
-        }
-        if (lane == 0) mi[hq] = make_float2(M == -INFINITY ? 0.f : M, L == 0.f ? 0.f : 1.f / L);
+        const float2 ML = join(a, p, pp, x, r, hq, lane);
+        if (lane == 0) mi[hq] = make_float2(ML.x, ML.y == 0.f ? 0.f : 1.f / ML.y);
     }
     __syncthreads();
     if (j >= a.k) return;
@@ -468,8 +491,13 @@ cudaError_t launch_rows(const GroupArgs &a, const RowsPlan &p, bool overlap, cud
 
 cudaError_t launch_merge(const GroupArgs &a, const RowsPlan &p, const PrefixPlan &pp,
                          cudaStream_t st) {
+    constexpr int kWarps = kMergeThreads / 32;
+    // warps to an output: a round of four loads each, about
+    const int64_t rows_parts_each = p.total > 0 ? ((int64_t)p.ctas / a.n_req + 2) * p.subs : 0;
+    int share = 1;
+    while (share < kWarps && pp.splits + rows_parts_each > 4 * share) share *= 2;
     const int64_t units = (int64_t)a.n_req * a.q_heads;
-    const int out_blocks = (int)((units + kMergeThreads / 32 - 1) / (kMergeThreads / 32));
+    const int out_blocks = (int)((units * share + kWarps - 1) / kWarps);
     const int64_t weight_blocks =
         a.weights ? (int64_t)a.n_req * ((a.k + kMergeThreads - 1) / kMergeThreads) : 0;
     cudaLaunchConfig_t cfg = {};
@@ -481,7 +509,7 @@ cudaError_t launch_merge(const GroupArgs &a, const RowsPlan &p, const PrefixPlan
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, merge_kernel, a, p, pp, out_blocks);
+    return cudaLaunchKernelEx(&cfg, merge_kernel, a, p, pp, out_blocks, share);
 }
 
 }  // namespace

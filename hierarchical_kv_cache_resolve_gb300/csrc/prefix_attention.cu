@@ -51,16 +51,15 @@ constexpr int kBlock = 128;                     // keys per block, rows per tile
 constexpr uint32_t kTileBytes = kBlock * kDim * 2;  // 32 KB
 constexpr uint32_t kAtom = kBlock * 128;        // 64 of the 128 dimensions: 16 KB
 constexpr int kSlots = 5;
-constexpr int kPrefixThreads = 320;
-constexpr int kRowThreads = 256;                // the two softmax groups
+constexpr int kPrefixThreads = 384;             // three warpgroups; the last two warps idle
 constexpr uint64_t kWaitLimitNs = 1000000000ull;
 constexpr float kRise = 8.f;                    // log2 of how far P may exceed 1
 
 constexpr uint32_t kOffQ = 0;                       // two tiles
 constexpr uint32_t kOffRing = 2 * kTileBytes;
 constexpr uint32_t kOffBar = kOffRing + kSlots * kTileBytes;
-// full[kSlots], empty[kSlots], s_full[2], p_ready[2], q_full, drained
-constexpr int kBars = 2 * kSlots + 6;
+// full[kSlots], empty[kSlots], s_full[2], p_half[2], p_ready[2], drained
+constexpr int kBars = 2 * kSlots + 7;
 constexpr uint32_t kOffWord = kOffBar + 8 * kBars;  // TMEM address, abort flag
 constexpr uint32_t kSmem = kOffWord + 16 + 1024;    // and room to align to 1 KB
 static_assert(kSmem <= 232448, "fits an SM");
@@ -192,6 +191,15 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t *v) {
         : "r"(addr));
 }
 
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, "
+        "%10, %11, %12, %13, %14, %15};" ::"r"(v[0]),
+        "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
+        "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(addr)
+        : "memory");
+}
+
 __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t *v) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, "
@@ -223,6 +231,19 @@ __device__ __forceinline__ void fence_after() {
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
 
+// two fp32 at once
+__device__ __forceinline__ uint64_t pair(uint32_t a, uint32_t b) { return (uint64_t)b << 32 | a; }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -241,30 +262,42 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     auto full = [&](int i) { return bars + 8u * i; };
     auto empty = [&](int i) { return bars + 8u * (kSlots + i); };
     auto s_full = [&](int t) { return bars + 8u * (2 * kSlots + t); };
-    auto p_ready = [&](int t) { return bars + 8u * (2 * kSlots + 2 + t); };
-    const uint32_t q_full = bars + 8u * (2 * kSlots + 4), drained = bars + 8u * (2 * kSlots + 5);
+    auto p_half = [&](int t) { return bars + 8u * (2 * kSlots + 2 + t); };
+    auto p_ready = [&](int t) { return bars + 8u * (2 * kSlots + 4 + t); };
+    const uint32_t drained = bars + 8u * (2 * kSlots + 6);
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     // the CTAs that read the same keys are neighbours
     const int pairs = (p.row_tiles + 1) / 2;
-    const int pair = blockIdx.x % pairs, head = (blockIdx.x / pairs) % a.heads;
+    const int pair_id = blockIdx.x % pairs, head = (blockIdx.x / pairs) % a.heads;
     const int split = blockIdx.x / pairs / a.heads;
     const int group = a.q_heads / a.heads;
     const int64_t n_rows = (int64_t)a.n_req * group;
     // one tile: its two halves of the blocks go to the two groups
-    const bool alone = 2 * pair + 1 == p.row_tiles;
+    const bool alone = 2 * pair_id + 1 == p.row_tiles;
     const int b0 = (int)((int64_t)split * p.blocks / p.splits);
     const int b1 = (int)((int64_t)(split + 1) * p.blocks / p.splits);
     const int n = b1 - b0;  // >= 1
-    const int ahead = alone ? 2 : 1;
+    const int ahead = min(alone ? 2 : 1, n);
 
+    // The ring's items in the order the products use them: K of the first
+    // blocks, then V of block j and K of block j + ahead.
+    auto load = [&](int i) {
+        const int u = i - ahead, both = 2 * (n - ahead);  // both: V, K, V, K, ...; then V only
+        const bool is_k = u < 0 || (u < both && (u & 1));
+        const int block = u < 0 ? i : u < both ? u / 2 + (u & 1 ? ahead : 0) : u - (n - ahead);
+        const int x = (is_k ? head : a.heads + head) * kDim, slot = i % kSlots;
+        const uint32_t dst = s0 + kOffRing + slot * kTileBytes;
+        mbar_expect(full(slot), kTileBytes);
+        tma_load(dst, &map, x, (b0 + block) * kBlock, full(slot));
+        tma_load(dst + kAtom, &map, x + 64, (b0 + block) * kBlock, full(slot));
+    };
     if (warp == 9) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
                          s0 + kOffWord)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
-    }
-    if (tid == 0) {
+    } else if (warp == 8 && lane == 0) {
         *abort_flag = 0;
         for (int i = 0; i < kSlots; ++i) {
             mbar_init(full(i), 1);
@@ -272,11 +305,37 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         }
         for (int t = 0; t < 2; ++t) {
             mbar_init(s_full(t), 1);
+            mbar_init(p_half(t), kBlock);
             mbar_init(p_ready(t), kBlock);
         }
-        mbar_init(q_full, kRowThreads);
         mbar_init(drained, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        for (int i = 0; i < kSlots && i < 2 * n; ++i) load(i);
+    }
+    // softmax groups: thread = row (TMEM lane) of tile t
+    const int t = (warp >> 2) & 1, row = tid & 127;
+    const int64_t m_row = (int64_t)(2 * pair_id + (alone ? 0 : t)) * kBlock + row;
+    const bool live = m_row < n_rows;
+    const int64_t q_row = live ? m_row / group * a.q_heads + head * group + m_row % group : 0;
+    // the queries' sign bits are turned for a negative scale; for scale 0 the
+    // queries become 0, so that a masked score stays -inf
+    const bool flat = a.scale_log2 == 0.f;
+    const float scale = flat ? 1.f : fabsf(a.scale_log2);
+    if (warp < 8 && (!alone || t == 0)) {
+        const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
+        const uint4 *src = reinterpret_cast<const uint4 *>(a.q + q_row * (2 * kDim));
+        uint8_t *dst = smem + kOffQ + t * kTileBytes + row * 128;
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+            uint4 x = live && !flat ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+            x.x ^= flip;
+            x.y ^= flip;
+            x.z ^= flip;
+            x.w ^= flip;
+            *reinterpret_cast<uint4 *>(dst + (c >> 3) * kAtom + (((c & 7) ^ (row & 7)) << 4)) = x;
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
     fence_before();
     __syncthreads();
@@ -284,39 +343,24 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     const uint32_t tmem = words[0];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
+    if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == 8) {
-        // ---- the ring: K of the first blocks, then V of block j and K of
-        // block j + ahead
+        // ---- the rest of the ring's items
         if (lane == 0) {
-            int i = 0;
-            bool ok = true;
-            auto load = [&](int block, int x) {
-                const int slot = i % kSlots;
-                if (i >= kSlots && !mbar_wait(empty(slot), (i / kSlots - 1) & 1, abort_flag)) {
-                    ok = false;
-                    return;
-                }
-                const uint32_t dst = s0 + kOffRing + slot * kTileBytes;
-                mbar_expect(full(slot), kTileBytes);
-                tma_load(dst, &map, x, block * kBlock, full(slot));
-                tma_load(dst + kAtom, &map, x + 64, block * kBlock, full(slot));
-                ++i;
-            };
-            const int kx = head * kDim, vx = (a.heads + head) * kDim;
-            for (int j = 0; j < ahead && j < n; ++j) load(b0 + j, kx);
-            for (int j = 0; j < n && ok; ++j) {
-                load(b0 + j, vx);
-                if (ok && j + ahead < n) load(b0 + j + ahead, kx);
+            int i = kSlots;
+            for (; i < 2 * n; ++i) {
+                if (!mbar_wait(empty(i % kSlots), (i / kSlots - 1) & 1, abort_flag)) break;
+                load(i);
             }
             // nothing may land after the CTA has left the ring (in a normal run
             // the products have waited for all of it)
-            for (int j = i > kSlots ? i - kSlots : 0; j < i; ++j)
+            const int issued = min(i, 2 * n);
+            for (int j = max(0, issued - kSlots); j < issued; ++j)
                 mbar_drain(full(j % kSlots), (j / kSlots) & 1);
         }
     } else if (warp == 9) {
         if (lane == 0) {
-            bool ok = mbar_wait(q_full, 0, abort_flag);
-            fence_after();
+            bool ok = true;
             int i = 0;
             auto arrived = [&](int item) {
                 const bool r = mbar_wait(full(item % kSlots), (item / kSlots) & 1, abort_flag);
@@ -333,12 +377,19 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                            c > 0);
                 }
             };
-            auto values = [&](int t, int item, bool add) {  // O_t += P_t V, 16 keys at a time
+            // O_t += P_t V, 16 keys at a time, each half of P as it is ready
+            auto values = [&](int t, int item, int turn, bool add) {
                 const uint32_t v = s0 + kOffRing + (item % kSlots) * kTileBytes;
 #pragma unroll
-                for (int c = 0; c < 8; ++c)
+                for (int c = 0; c < 8; ++c) {
+                    if (c == 0 || c == 4) {
+                        if (!mbar_wait(c ? p_ready(t) : p_half(t), turn & 1, abort_flag)) return false;
+                        fence_after();
+                    }
                     mma_ts(tmem + 256 + t * 128, tmem + t * 128 + c * 8,
                            operand(v + c * 2048, kAtom), kIdescV, add || c > 0);
+                }
+                return true;
             };
             if (alone) {
                 for (int j = 0; j < 2 && j < n && ok; ++j) {
@@ -350,9 +401,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                 }
                 for (int j = 0; j < n && ok; ++j) {
                     const int t = j & 1;
-                    if (!(ok = mbar_wait(p_ready(t), (j >> 1) & 1, abort_flag))) break;
                     if (!(ok = arrived(i))) break;
-                    values(t, i, j >= 2);
+                    if (!(ok = values(t, i, j >> 1, j >= 2))) break;
                     mma_commit(empty(i % kSlots));
                     ++i;
                     if (j + 2 < n) {
@@ -375,9 +425,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                 for (int j = 0; j < n && ok; ++j) {
                     const bool more = j + 1 < n;
                     for (int t = 0; t < 2; ++t) {
-                        if (!(ok = mbar_wait(p_ready(t), j & 1, abort_flag))) break;
                         if (t == 0 && !(ok = arrived(i))) break;
-                        values(t, i, j > 0);
+                        if (!(ok = values(t, i, j, j > 0))) break;
                         if (t == 1) mma_commit(empty(i % kSlots));
                         if (more) {
                             if (t == 0 && !(ok = arrived(i + 1))) break;
@@ -393,34 +442,9 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
             mma_commit(drained);
             mbar_drain(drained, 0);
         }
-    } else {
-        // ---- softmax: thread = row (TMEM lane) of tile t
-        const int t = warp >> 2, row = tid & 127;
-        const int64_t m_row = (int64_t)(2 * pair + (alone ? 0 : t)) * kBlock + row;
-        const bool live = m_row < n_rows;
-        const int64_t q_row =
-            live ? m_row / group * a.q_heads + head * group + m_row % group : 0;
-        // the queries' sign bits are turned for a negative scale; for scale 0
-        // the queries become 0, so that a masked score stays -inf
-        const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
-        const bool flat = a.scale_log2 == 0.f;
-        const float scale = flat ? 1.f : fabsf(a.scale_log2);
-        if (!alone || t == 0) {
-            const uint4 *src = reinterpret_cast<const uint4 *>(a.q + q_row * (2 * kDim));
-            uint8_t *dst = smem + kOffQ + t * kTileBytes + row * 128;
-#pragma unroll
-            for (int c = 0; c < 16; ++c) {
-                uint4 x = live && !flat ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
-                x.x ^= flip;
-                x.y ^= flip;
-                x.z ^= flip;
-                x.w ^= flip;
-                *reinterpret_cast<uint4 *>(dst + (c >> 3) * kAtom + (((c & 7) ^ (row & 7)) << 4)) = x;
-            }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        }
-        mbar_arrive(q_full);
-
+    } else if (warp < 8) {
+        // ---- softmax
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
         const uint32_t lanes = (uint32_t)(warp & 3) * 32 << 16;
         const uint32_t ts = tmem + lanes + t * 128, to = tmem + lanes + 256 + t * 128;
         // blocks b0 + first, + step, ...
@@ -435,21 +459,26 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                 break;
             }
             fence_after();
-            uint32_t s[128];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_ld32(ts + c * 32, s + c * 32);
-            tmem_wait_ld<128>(s);
             const int64_t left = a.prefix_len - (int64_t)(b0 + first + j * step) * kBlock;
-            if (left < kBlock) {
+            uint32_t s[128];
+            float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            tmem_ld32(ts, s);
 #pragma unroll
-                for (int c = 0; c < 128; ++c)
-                    if (c >= (int)left) s[c] = 0xFF800000u;  // -inf behind the prefix
+            for (int c = 0; c < 4; ++c) {
+                tmem_wait_ld<32>(s + c * 32);
+                if (c < 3) tmem_ld32(ts + (c + 1) * 32, s + (c + 1) * 32);
+                if (left < kBlock) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (c * 32 + e >= (int)left) s[c * 32 + e] = 0xFF800000u;  // -inf
+                }
+#pragma unroll
+                for (int e = 0; e < 32; e += 8)
+#pragma unroll
+                    for (int h = 0; h < 4; ++h)
+                        x[h] = fmaxf(fmaxf(x[h], __uint_as_float(s[c * 32 + e + 2 * h])),
+                                     __uint_as_float(s[c * 32 + e + 2 * h + 1]));
             }
-            float x[4];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) x[c] = __uint_as_float(s[c]);
-#pragma unroll
-            for (int c = 4; c < 128; ++c) x[c & 3] = fmaxf(x[c & 3], __uint_as_float(s[c]));
             const float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * scale;
             if (__any_sync(0xFFFFFFFFu, top > m + kRise || m == -INFINITY)) {
                 const float up = fmaxf(m, top);
@@ -458,7 +487,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                 l *= f;
                 if (j > 0) {  // s_full came after the products on O
                     uint32_t o[32];
-#pragma unroll
+#pragma unroll 1
                     for (int c = 0; c < 4; ++c) {
                         tmem_ld32(to + c * 32, o);
                         tmem_wait_ld<32>(o);
@@ -470,22 +499,29 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                 }
             }
             const float shift = m == -INFINITY ? 0.f : -m;
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};
-            uint32_t pk[64];
+            const uint64_t scale2 = pair(__float_as_uint(scale), __float_as_uint(scale));
+            const uint64_t shift2 = pair(__float_as_uint(shift), __float_as_uint(shift));
+            uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
-            for (int c = 0; c < 64; ++c) {
-                const float p0 = ex2(fmaf(__uint_as_float(s[2 * c]), scale, shift));
-                const float p1 = ex2(fmaf(__uint_as_float(s[2 * c + 1]), scale, shift));
-                sum[c & 1] += p0;
-                sum[2 + (c & 1)] += p1;
-                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(pk[c]) : "f"(p1), "f"(p0));
+            for (int c = 0; c < 4; ++c) {
+                uint32_t pk[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const uint64_t y = fma2(pair(s[c * 32 + 2 * e], s[c * 32 + 2 * e + 1]), scale2, shift2);
+                    const float p0 = ex2(__uint_as_float((uint32_t)y));
+                    const float p1 = ex2(__uint_as_float((uint32_t)(y >> 32)));
+                    sum[e & 1] = add2(sum[e & 1], pair(__float_as_uint(p0), __float_as_uint(p1)));
+                    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(pk[e]) : "f"(p1), "f"(p0));
+                }
+                tmem_st16(ts + c * 16, pk);
+                if (c & 1) {
+                    tmem_wait_st();
+                    fence_before();
+                    mbar_arrive(c == 1 ? p_half(t) : p_ready(t));
+                }
             }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-            tmem_st32(ts, pk);
-            tmem_st32(ts + 32, pk + 32);
-            tmem_wait_st();
-            fence_before();
-            mbar_arrive(p_ready(t));
+            sum[0] = add2(sum[0], sum[1]);
+            l += __uint_as_float((uint32_t)sum[0]) + __uint_as_float((uint32_t)(sum[0] >> 32));
         }
         // every product on O done
         if (ok && mine > 0) {
