@@ -138,10 +138,11 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *map, i
 
 // Shared-memory matrix descriptor, 128-byte swizzle: address, the strides
 // between 64-element chunks of a row-contiguous operand (lead) and between
-// groups of eight 128-byte rows (1 KB), all in 16-byte units.
+// groups of eight 128-byte rows (1 KB), all in 16-byte units.  The address is
+// below 2^18, so bytes / 16 may be added to a descriptor.
 __device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lead) {
-    return (uint64_t)((addr >> 4) & 0x3FFF) | (uint64_t)((lead >> 4) & 0x3FFF) << 16 |
-           (uint64_t)(1024 >> 4) << 32 | 1ull << 46 | 2ull << 61;
+    return (uint64_t)(addr >> 4) | (uint64_t)(lead >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
+           1ull << 46 | 2ull << 61;
 }
 
 // fp32 accumulators, bf16 operands, N = 128, M = 128; bit 16: B is given with
@@ -167,6 +168,17 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
         "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
         : "memory");
+}
+
+// One lane of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xFFFFFFFF;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r != 0;
 }
 
 // `bar` gets an arrival once every product issued so far by this thread is done
@@ -266,7 +278,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     auto p_ready = [&](int t) { return bars + 8u * (2 * kSlots + 4 + t); };
     const uint32_t drained = bars + 8u * (2 * kSlots + 6);
 
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);  // known to be the same in a warp
     // the CTAs that read the same keys are neighbours
     const int pairs = (p.row_tiles + 1) / 2;
     const int pair_id = blockIdx.x % pairs, head = (blockIdx.x / pairs) % a.heads;
@@ -359,89 +372,113 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                 mbar_drain(full(j % kSlots), (j / kSlots) & 1);
         }
     } else if (warp == 9) {
-        if (lane == 0) {
-            bool ok = true;
-            int i = 0;
-            auto arrived = [&](int item) {
-                const bool r = mbar_wait(full(item % kSlots), (item / kSlots) & 1, abort_flag);
-                fence_after();
-                return r;
-            };
-            auto scores = [&](int t, int item) {  // S_t = Q_t K^T, 16 dimensions at a time
-                const uint32_t q = s0 + kOffQ + (alone ? 0 : t) * kTileBytes;
-                const uint32_t k = s0 + kOffRing + (item % kSlots) * kTileBytes;
+        // ---- the products: the whole warp waits, one lane issues
+        const bool issuer = elect_one();
+        bool ok = true;
+        const uint64_t q_op = operand(s0 + kOffQ, 16);
+        const uint64_t k_op = operand(s0 + kOffRing, 16), v_op = operand(s0 + kOffRing, kAtom);
+        int slot = 0;                       // of the next item, and its phase
+        uint32_t phase = 0;
+        auto next = [&]() {
+            if (++slot == kSlots) {
+                slot = 0;
+                phase ^= 1;
+            }
+        };
+        auto arrived = [&](int at, uint32_t ph) {
+            const bool r = mbar_wait(full(at), ph, abort_flag);
+            fence_after();
+            return r;
+        };
+        auto commit = [&](uint32_t bar) {
+            if (issuer) mma_commit(bar);
+        };
+        // S_t = Q_t K^T, 16 dimensions at a time
+        auto scores = [&](int tile, int at) {
+            const uint64_t q = q_op + (alone ? 0 : tile) * (kTileBytes >> 4);
+            const uint64_t k = k_op + at * (kTileBytes >> 4);
+            const uint32_t d = tmem + tile * 128;
+            if (issuer) {
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
-                    const uint32_t off = (c >> 2) * kAtom + (c & 3) * 32;
-                    mma_ss(tmem + t * 128, operand(q + off, 16), operand(k + off, 16), kIdesc,
-                           c > 0);
-                }
-            };
-            // O_t += P_t V, 16 keys at a time, each half of P as it is ready
-            auto values = [&](int t, int item, int turn, bool add) {
-                const uint32_t v = s0 + kOffRing + (item % kSlots) * kTileBytes;
-#pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    if (c == 0 || c == 4) {
-                        if (!mbar_wait(c ? p_ready(t) : p_half(t), turn & 1, abort_flag)) return false;
-                        fence_after();
-                    }
-                    mma_ts(tmem + 256 + t * 128, tmem + t * 128 + c * 8,
-                           operand(v + c * 2048, kAtom), kIdescV, add || c > 0);
-                }
-                return true;
-            };
-            if (alone) {
-                for (int j = 0; j < 2 && j < n && ok; ++j) {
-                    if (!(ok = arrived(i))) break;
-                    scores(j, i);
-                    mma_commit(s_full(j));
-                    mma_commit(empty(i % kSlots));
-                    ++i;
-                }
-                for (int j = 0; j < n && ok; ++j) {
-                    const int t = j & 1;
-                    if (!(ok = arrived(i))) break;
-                    if (!(ok = values(t, i, j >> 1, j >= 2))) break;
-                    mma_commit(empty(i % kSlots));
-                    ++i;
-                    if (j + 2 < n) {
-                        if (!(ok = arrived(i))) break;
-                        scores(t, i);
-                        mma_commit(empty(i % kSlots));
-                        ++i;
-                    }
-                    mma_commit(s_full(t));
-                }
-            } else {
-                if (ok && (ok = arrived(i))) {
-                    for (int t = 0; t < 2; ++t) {
-                        scores(t, i);
-                        mma_commit(s_full(t));
-                    }
-                    mma_commit(empty(i % kSlots));
-                    ++i;
-                }
-                for (int j = 0; j < n && ok; ++j) {
-                    const bool more = j + 1 < n;
-                    for (int t = 0; t < 2; ++t) {
-                        if (t == 0 && !(ok = arrived(i))) break;
-                        if (!(ok = values(t, i, j, j > 0))) break;
-                        if (t == 1) mma_commit(empty(i % kSlots));
-                        if (more) {
-                            if (t == 0 && !(ok = arrived(i + 1))) break;
-                            scores(t, i + 1);
-                            if (t == 1) mma_commit(empty((i + 1) % kSlots));
-                        }
-                        mma_commit(s_full(t));
-                    }
-                    i += more ? 2 : 1;
+                    const uint64_t off = ((c >> 2) * kAtom + (c & 3) * 32) >> 4;
+                    mma_ss(d, q + off, k + off, kIdesc, c > 0);
                 }
             }
-            // no product may still run when the TMEM is given back
-            mma_commit(drained);
-            mbar_drain(drained, 0);
+        };
+        // O_t += P_t V, 16 keys at a time, each half of P as it is ready
+        auto values = [&](int tile, int at, int turn, bool add) {
+            const uint64_t v = v_op + at * (kTileBytes >> 4);
+            const uint32_t pt = tmem + tile * 128, d = tmem + 256 + tile * 128;
+            if (!mbar_wait(p_half(tile), turn & 1, abort_flag)) return false;
+            fence_after();
+            if (issuer) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    mma_ts(d, pt + c * 8, v + c * (2048 >> 4), kIdescV, add || c > 0);
+            }
+            if (!mbar_wait(p_ready(tile), turn & 1, abort_flag)) return false;
+            fence_after();
+            if (issuer) {
+#pragma unroll
+                for (int c = 4; c < 8; ++c)
+                    mma_ts(d, pt + c * 8, v + c * (2048 >> 4), kIdescV, true);
+            }
+            return true;
+        };
+        if (alone) {
+            for (int j = 0; j < ahead && ok; ++j) {
+                if (!(ok = arrived(slot, phase))) break;
+                scores(j, slot);
+                commit(s_full(j));
+                commit(empty(slot));
+                next();
+            }
+            for (int j = 0; j < n && ok; ++j) {
+                const int tile = j & 1;
+                if (!(ok = arrived(slot, phase))) break;
+                if (!(ok = values(tile, slot, j >> 1, j >= 2))) break;
+                commit(empty(slot));
+                next();
+                if (j + 2 < n) {
+                    if (!(ok = arrived(slot, phase))) break;
+                    scores(tile, slot);
+                    commit(empty(slot));
+                    next();
+                }
+                commit(s_full(tile));
+            }
+        } else {
+            if ((ok = arrived(slot, phase))) {
+                for (int tile = 0; tile < 2; ++tile) {
+                    scores(tile, slot);
+                    commit(s_full(tile));
+                }
+                commit(empty(slot));
+                next();
+            }
+            for (int j = 0; j < n && ok; ++j) {
+                const bool more = j + 1 < n;
+                const int v_slot = slot;
+                const uint32_t v_phase = phase;
+                next();
+                for (int tile = 0; tile < 2; ++tile) {
+                    if (tile == 0 && !(ok = arrived(v_slot, v_phase))) break;
+                    if (!(ok = values(tile, v_slot, j, j > 0))) break;
+                    if (tile == 1) commit(empty(v_slot));
+                    if (more) {
+                        if (tile == 0 && !(ok = arrived(slot, phase))) break;
+                        scores(tile, slot);
+                        if (tile == 1) commit(empty(slot));
+                    }
+                    commit(s_full(tile));
+                }
+                if (more) next();
+            }
         }
+        // no product may still run when the TMEM is given back
+        commit(drained);
+        mbar_drain(drained, 0);
     } else if (warp < 8) {
         // ---- softmax
         asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
