@@ -309,22 +309,41 @@ constexpr int kSms = 152;  // the SMs that work is split over, whatever device a
 struct RowsPlan {
     int32_t tiles, subs, ctas;
     int64_t total;
+    int64_t each;   // total / ctas
+    int32_t rest;   // total % ctas
+    int32_t lead;   // (ctas - 1) / tiles
     float *o;
     float2 *ml;
 };
-// A split of the prefix: part s holds n_req * q_heads rows.
+// A split of the prefix: `groups` ranges of the heads * blocks key blocks,
+// head after head; a group is a CTA for every pair of row tiles.  The part of
+// (group g, head h) is g + h, of n_req * (q_heads / heads) rows.
 struct PrefixPlan {
-    int32_t splits, blocks, row_tiles;
+    int32_t groups, blocks, row_tiles;
+    int32_t total;  // heads * blocks
+    int32_t lead;   // (groups - 1) / blocks
     float *o;
     float2 *ml;
 };
+// Range c of n equal ranges of `total` things starts at c * total / n, here
+// from each = total / n and rest = total % n (64-bit divisions take a thread
+// the better part of a microsecond).
+template <class T>
+__host__ __device__ inline T range_start(int c, int n, T each, int rest) {
+    return (T)c * each + c * rest / n;
+}
+__host__ __device__ inline int64_t quick_div(int64_t a, int b) {
+    return a >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
+}
 size_t prefix_attention_bytes(int n_req, int q_heads, int heads, int64_t prefix_len, int k);
 size_t attention_weights_bytes(int n_req, int q_heads, int heads, int k);
 cudaError_t launch_prefix_attention(GroupArgs a, void *work, cudaStream_t st);
 cudaError_t launch_attention_weights(GroupArgs a, void *work, cudaStream_t st);
 // prefix_attention.cu
-PrefixPlan prefix_plan(int n_req, int q_heads, int heads, int64_t prefix_len);
-cudaError_t launch_prefix(const GroupArgs &a, const PrefixPlan &p, cudaStream_t st);
+PrefixPlan prefix_plan(int n_req, int q_heads, int heads, int64_t prefix_len, int ctas);
+// the prefix's parts, and beside them the rows' (rows.total > 0) on CTAs of their own
+cudaError_t launch_prefix(const GroupArgs &a, const PrefixPlan &p, const RowsPlan &rows,
+                          cudaStream_t st);
 cudaError_t prefix_attention_status(uint32_t *status);
 
 // select_heavy.cu: hs_select_heavy

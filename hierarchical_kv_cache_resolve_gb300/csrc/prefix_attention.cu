@@ -8,10 +8,13 @@
 // 4 * 128 * R g flops for 512 bytes: bound by HBM below about R g = 70, by
 // the tensor cores above a few hundred.
 //
-// Work split: a CTA takes one key-value head, up to two tiles of 128 rows and
-// a contiguous range of 128-key blocks; the ranges are cut so that the grid
-// covers the 152 SMs once, and merge_kernel joins their parts.  One CTA per
-// SM:
+// Work split: the key blocks of 128 of all key-value heads, head after head,
+// are cut into equal contiguous ranges, one for each group of CTAs; the CTAs
+// of a group take the same range (their reads meet in L2) for a pair of row
+// tiles of 128 each.  The first CTAs of the grid take the requests' own rows
+// instead (rows_gather.cuh): the two share the GPU at once, so the rows' reads
+// use the bandwidth that the products leave and neither waits for the other's
+// last CTA.  merge_kernel joins all parts.  One CTA per SM:
 //   warp 8    brings key and value blocks (32 KB each, TMA, 128-byte swizzle)
 //             into a ring of five, in the order the products use them;
 //   warp 9    one thread issues S_t = Q_t K^T and O_t += P_t V;
@@ -22,7 +25,7 @@
 // While one tile's softmax runs, the tensor core works on the other's
 // products.  With a single tile of rows (few queries, bound by HBM) the two
 // softmax groups take every other key block of the same rows, and the two
-// results are joined in shared memory at the end.
+// results are joined in shared memory behind the last block of a head.
 //
 // The maximum only rises when a block exceeds it by more than 2^8: until then
 // P is at most 2^8 too large, which bf16 and the fp32 sums hold as exactly,
@@ -42,6 +45,7 @@
 
 #include "hs.h"
 #include "hs_internal.cuh"
+#include "rows_gather.cuh"
 
 namespace hs {
 namespace {
@@ -58,14 +62,17 @@ constexpr float kRise = 8.f;                    // log2 of how far P may exceed 
 constexpr uint32_t kOffQ = 0;                       // two tiles
 constexpr uint32_t kOffRing = 2 * kTileBytes;
 constexpr uint32_t kOffBar = kOffRing + kSlots * kTileBytes;
-// full[kSlots], empty[kSlots], s_full[2], p_half[2], p_ready[2], drained
-constexpr int kBars = 2 * kSlots + 7;
+// full[kSlots], empty[kSlots], s_full[2], p_half[2], p_ready[2], q_full, drained
+constexpr int kBars = 2 * kSlots + 8;
 constexpr uint32_t kOffWord = kOffBar + 8 * kBars;  // TMEM address, abort flag
-constexpr uint32_t kSmem = kOffWord + 16 + 1024;    // and room to align to 1 KB
+// with one tile of rows: both groups' (m, l) [2][128]; half of each group's O
+// goes to the other through the query tiles' places
+constexpr uint32_t kOffXml = kOffWord + 16;
+constexpr uint32_t kSmem = kOffXml + 2 * kBlock * 8;
 static_assert(kSmem <= 232448, "fits an SM");
-// after the main loop the ring holds the second group's O [32 chunks][128
-// rows] of float4 and (m, l) [128]
-static_assert(kTileBytes * 2 + kBlock * 8 <= kSlots * kTileBytes, "the exchange fits the ring");
+static_assert(kOffBar % 8 == 0 && kOffXml % 8 == 0, "barriers and (m, l) are 8-byte aligned");
+static_assert(64 * kBlock * 4 <= kTileBytes, "half of O fits a query tile's place");
+static_assert(rows::kMaxWarps * rows::kWarpSmem <= kSmem, "the row CTAs' rings fit");
 
 __device__ uint32_t g_prefix_status;
 
@@ -243,6 +250,25 @@ __device__ __forceinline__ void fence_after() {
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
 
+// 32 bytes to a 32-byte boundary
+__device__ __forceinline__ void store32(float *p, const uint32_t *v) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]),
+                 "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
+__device__ __forceinline__ void st_shared16(uint32_t addr, const uint32_t *v) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]),
+                 "r"(v[2]), "r"(v[3])
+                 : "memory");
+}
+__device__ __forceinline__ void ld_shared16(uint32_t addr, uint32_t *v) {
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
 // two fp32 at once
 __device__ __forceinline__ uint64_t pair(uint32_t a, uint32_t b) { return (uint64_t)b << 32 | a; }
 __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
@@ -263,10 +289,21 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 __global__ void __launch_bounds__(kPrefixThreads, 1)
-    prefix_kernel(const __grid_constant__ CUtensorMap map, const GroupArgs a, const PrefixPlan p) {
-    extern __shared__ uint8_t smem_raw[];
-    const uint32_t raw = smem_addr(smem_raw);
-    uint8_t *smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+    prefix_kernel(const __grid_constant__ CUtensorMap map, const GroupArgs a, const PrefixPlan p,
+                  const RowsPlan rp) {
+    extern __shared__ __align__(1024) uint8_t smem[];  // the swizzle's period
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);  // known to be the same in a warp
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if ((int)blockIdx.x < rp.ctas) {  // (0 without own rows)
+        if (warp >= 8) {
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        } else {
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+            if (warp < a.heads * rp.subs) rows::gather_rows<false>(a, rp, blockIdx.x, smem);
+        }
+        return;
+    }
     const uint32_t s0 = smem_addr(smem);
     volatile uint32_t *words = reinterpret_cast<volatile uint32_t *>(smem + kOffWord);
     volatile uint32_t *abort_flag = words + 1;
@@ -276,34 +313,38 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     auto s_full = [&](int t) { return bars + 8u * (2 * kSlots + t); };
     auto p_half = [&](int t) { return bars + 8u * (2 * kSlots + 2 + t); };
     auto p_ready = [&](int t) { return bars + 8u * (2 * kSlots + 4 + t); };
-    const uint32_t drained = bars + 8u * (2 * kSlots + 6);
+    const uint32_t q_full = bars + 8u * (2 * kSlots + 6), drained = bars + 8u * (2 * kSlots + 7);
 
-    const int tid = threadIdx.x, lane = tid & 31;
-    const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);  // known to be the same in a warp
     // the CTAs that read the same keys are neighbours
     const int pairs = (p.row_tiles + 1) / 2;
-    const int pair_id = blockIdx.x % pairs, head = (blockIdx.x / pairs) % a.heads;
-    const int split = blockIdx.x / pairs / a.heads;
+    const int cta = (int)blockIdx.x - rp.ctas;
+    const int pair_id = cta % pairs, g = cta / pairs;
     const int group = a.q_heads / a.heads;
-    const int64_t n_rows = (int64_t)a.n_req * group;
-    // one tile: its two halves of the blocks go to the two groups
+    const int n_rows = a.n_req * group;  // at most 65535 * 16
+    // one tile: its blocks go to the two groups in turn
     const bool alone = 2 * pair_id + 1 == p.row_tiles;
-    const int b0 = (int)((int64_t)split * p.blocks / p.splits);
-    const int b1 = (int)((int64_t)(split + 1) * p.blocks / p.splits);
-    const int n = b1 - b0;  // >= 1
-    const int ahead = min(alone ? 2 : 1, n);
+    const int each = p.total / p.groups, rest = p.total % p.groups;
+    const int t0 = range_start(g, p.groups, each, rest), t1 = range_start(g + 1, p.groups, each, rest);
+    const int head0 = t0 / p.blocks, head1 = (t1 - 1) / p.blocks;
+    // blocks [first, first + n) of a head are this group's; n >= 1
+    auto first_block = [&](int head) { return max(0, t0 - head * p.blocks); };
+    auto count = [&](int head) { return min(p.blocks, t1 - head * p.blocks) - first_block(head); };
+    // how many blocks' keys come before the first block's values
+    auto ahead_of = [&](int n) { return min(alone ? 2 : 1, n); };
 
-    // The ring's items in the order the products use them: K of the first
-    // blocks, then V of block j and K of block j + ahead.
-    auto load = [&](int i) {
+    // A head's items of the ring in the order the products use them: K of the
+    // first blocks, then V of block j and K of block j + ahead.
+    auto load = [&](int item, int head, int i) {
+        const int n = count(head), ahead = ahead_of(n);
         const int u = i - ahead, both = 2 * (n - ahead);  // both: V, K, V, K, ...; then V only
         const bool is_k = u < 0 || (u < both && (u & 1));
         const int block = u < 0 ? i : u < both ? u / 2 + (u & 1 ? ahead : 0) : u - (n - ahead);
-        const int x = (is_k ? head : a.heads + head) * kDim, slot = i % kSlots;
+        const int x = (is_k ? head : a.heads + head) * kDim, slot = item % kSlots;
+        const int y = (first_block(head) + block) * kBlock;
         const uint32_t dst = s0 + kOffRing + slot * kTileBytes;
         mbar_expect(full(slot), kTileBytes);
-        tma_load(dst, &map, x, (b0 + block) * kBlock, full(slot));
-        tma_load(dst + kAtom, &map, x + 64, (b0 + block) * kBlock, full(slot));
+        tma_load(dst, &map, x, y, full(slot));
+        tma_load(dst + kAtom, &map, x + 64, y, full(slot));
     };
     if (warp == 9) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
@@ -321,318 +362,321 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
             mbar_init(p_half(t), kBlock);
             mbar_init(p_ready(t), kBlock);
         }
+        mbar_init(q_full, 2 * kBlock);
         mbar_init(drained, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        for (int i = 0; i < kSlots && i < 2 * n; ++i) load(i);
+        // two items before the queries' loads, which the rest would delay
+        load(0, head0, 0);
+        load(1, head0, 1);
     }
     // softmax groups: thread = row (TMEM lane) of tile t
     const int t = (warp >> 2) & 1, row = tid & 127;
-    const int64_t m_row = (int64_t)(2 * pair_id + (alone ? 0 : t)) * kBlock + row;
+    const int m_row = (2 * pair_id + (alone ? 0 : t)) * kBlock + row;
     const bool live = m_row < n_rows;
-    const int64_t q_row = live ? m_row / group * a.q_heads + head * group + m_row % group : 0;
     // the queries' sign bits are turned for a negative scale; for scale 0 the
     // queries become 0, so that a masked score stays -inf
     const bool flat = a.scale_log2 == 0.f;
     const float scale = flat ? 1.f : fabsf(a.scale_log2);
-    if (warp < 8 && (!alone || t == 0)) {
+    auto load_q = [&](int head) {
+        if (alone && t == 1) return;
         const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
-        const uint4 *src = reinterpret_cast<const uint4 *>(a.q + q_row * (2 * kDim));
-        uint8_t *dst = smem + kOffQ + t * kTileBytes + row * 128;
+        // a warp's 32 rows, two at a time: 16 lanes to a row of 256 bytes
+        const int c = lane & 15;
+        uint8_t *dst = smem + kOffQ + t * kTileBytes + (c >> 3) * kAtom;
 #pragma unroll
-        for (int c = 0; c < 16; ++c) {
-            uint4 x = live && !flat ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+        for (int i = 0; i < 16; ++i) {
+            const int at = (warp & 3) * 32 + 2 * i + (lane >> 4);
+            const int m_at = m_row - row + at;
+            uint4 x = make_uint4(0u, 0u, 0u, 0u);
+            if (m_at < n_rows && !flat) {
+                const int q_row = m_at / group * a.q_heads + head * group + m_at % group;
+                x = __ldg(reinterpret_cast<const uint4 *>(a.q + (int64_t)q_row * (2 * kDim)) + c);
+            }
             x.x ^= flip;
             x.y ^= flip;
             x.z ^= flip;
             x.w ^= flip;
-            *reinterpret_cast<uint4 *>(dst + (c >> 3) * kAtom + (((c & 7) ^ (row & 7)) << 4)) = x;
+            *reinterpret_cast<uint4 *>(dst + at * 128 + (((c & 7) ^ (at & 7)) << 4)) = x;
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    }
+    };
+    if (warp < 8) load_q(head0);
     fence_before();
     __syncthreads();
     fence_after();
     const uint32_t tmem = words[0];
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == 8) {
         // ---- the rest of the ring's items
         if (lane == 0) {
-            int i = kSlots;
-            for (; i < 2 * n; ++i) {
-                if (!mbar_wait(empty(i % kSlots), (i / kSlots - 1) & 1, abort_flag)) break;
-                load(i);
-            }
+            int item = 0;
+            bool ok = true;
+            for (int head = head0; head <= head1 && ok; ++head)
+                for (int i = 0, n = 2 * count(head); i < n; ++i, ++item) {
+                    if (head == head0 && i < 2) continue;  // above
+                    if (item >= kSlots &&
+                        !(ok = mbar_wait(empty(item % kSlots), (item / kSlots - 1) & 1, abort_flag)))
+                        break;
+                    load(item, head, i);
+                }
             // nothing may land after the CTA has left the ring (in a normal run
             // the products have waited for all of it)
-            const int issued = min(i, 2 * n);
-            for (int j = max(0, issued - kSlots); j < issued; ++j)
+            for (int j = max(0, item - kSlots); j < item; ++j)
                 mbar_drain(full(j % kSlots), (j / kSlots) & 1);
         }
     } else if (warp == 9) {
         // ---- the products: the whole warp waits, one lane issues
         const bool issuer = elect_one();
-        bool ok = true;
         const uint64_t q_op = operand(s0 + kOffQ, 16);
         const uint64_t k_op = operand(s0 + kOffRing, 16), v_op = operand(s0 + kOffRing, kAtom);
-        int slot = 0;                       // of the next item, and its phase
-        uint32_t phase = 0;
-        auto next = [&]() {
-            if (++slot == kSlots) {
-                slot = 0;
-                phase ^= 1;
-            }
-        };
-        auto arrived = [&](int at, uint32_t ph) {
-            const bool r = mbar_wait(full(at), ph, abort_flag);
+        int item = 0;                       // the next item of the ring
+        uint32_t p_phase = 0;               // bit t: of P_t
+        bool ok = true;
+        auto arrived = [&](int i) {
+            ok = mbar_wait(full(i % kSlots), (i / kSlots) & 1, abort_flag);
             fence_after();
-            return r;
-        };
-        auto commit = [&](uint32_t bar) {
-            if (issuer) mma_commit(bar);
+            return ok;
         };
         // S_t = Q_t K^T, 16 dimensions at a time
-        auto scores = [&](int tile, int at) {
-            const uint64_t q = q_op + (alone ? 0 : tile) * (kTileBytes >> 4);
-            const uint64_t k = k_op + at * (kTileBytes >> 4);
-            const uint32_t d = tmem + tile * 128;
+        auto scores = [&](int tile, int i) {
+            const uint64_t q = q_op + (alone ? 0 : tile * (kTileBytes >> 4));
+            const uint64_t k = k_op + i % kSlots * (kTileBytes >> 4);
             if (issuer) {
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
                     const uint64_t off = ((c >> 2) * kAtom + (c & 3) * 32) >> 4;
-                    mma_ss(d, q + off, k + off, kIdesc, c > 0);
+                    mma_ss(tmem + tile * 128, q + off, k + off, kIdesc, c > 0);
                 }
             }
         };
-        // O_t += P_t V, 16 keys at a time, each half of P as it is ready
-        auto values = [&](int tile, int at, int turn, bool add) {
-            const uint64_t v = v_op + at * (kTileBytes >> 4);
-            const uint32_t pt = tmem + tile * 128, d = tmem + 256 + tile * 128;
-            if (!mbar_wait(p_half(tile), turn & 1, abort_flag)) return false;
+        for (int head = head0; head <= head1 && ok; ++head) {
+            const int n = count(head);
+            ok = mbar_wait(q_full, (head - head0) & 1, abort_flag);
             fence_after();
-            if (issuer) {
+            // the first scores of both tiles: of one block, or of two
+#pragma unroll 1
+            for (int tile = 0; tile < (alone ? min(n, 2) : 2) && ok; ++tile) {
+                if ((alone || tile == 0) && !arrived(item)) break;
+                scores(tile, item);
+                if (issuer) {
+                    mma_commit(s_full(tile));
+                    if (alone || tile == 1) mma_commit(empty(item % kSlots));
+                }
+                if (alone || tile == 1) ++item;
+            }
+            // then the tiles in turn: O_t += P_t V of a block, S_t of the next
+            const int turns = alone ? n : 2 * n;
+#pragma unroll 1
+            for (int u = 0; u < turns && ok; ++u) {
+                const int tile = u & 1, block = alone ? u : u >> 1;
+                const bool opens = alone || tile == 0, closes = alone || tile == 1;
+                const bool more = block + (alone ? 2 : 1) < n;
+                if (opens && !arrived(item)) break;
+                // 16 keys at a time, each half of P as it is ready
+                const uint64_t v = v_op + item % kSlots * (kTileBytes >> 4);
+                const uint32_t pt = tmem + tile * 128, d = tmem + 256 + tile * 128;
+                const uint32_t ph = p_phase >> tile & 1u;
+                if (!(ok = mbar_wait(p_half(tile), ph, abort_flag))) break;
+                fence_after();
+                if (issuer) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    mma_ts(d, pt + c * 8, v + c * (2048 >> 4), kIdescV, add || c > 0);
-            }
-            if (!mbar_wait(p_ready(tile), turn & 1, abort_flag)) return false;
-            fence_after();
-            if (issuer) {
+                    for (int c = 0; c < 4; ++c)
+                        mma_ts(d, pt + c * 8, v + c * (2048 >> 4), kIdescV,
+                               c > 0 || block >= (alone ? 2 : 1));
+                }
+                if (!(ok = mbar_wait(p_ready(tile), ph, abort_flag))) break;
+                fence_after();
+                if (issuer) {
 #pragma unroll
-                for (int c = 4; c < 8; ++c)
-                    mma_ts(d, pt + c * 8, v + c * (2048 >> 4), kIdescV, true);
-            }
-            return true;
-        };
-        if (alone) {
-            for (int j = 0; j < ahead && ok; ++j) {
-                if (!(ok = arrived(slot, phase))) break;
-                scores(j, slot);
-                commit(s_full(j));
-                commit(empty(slot));
-                next();
-            }
-            for (int j = 0; j < n && ok; ++j) {
-                const int tile = j & 1;
-                if (!(ok = arrived(slot, phase))) break;
-                if (!(ok = values(tile, slot, j >> 1, j >= 2))) break;
-                commit(empty(slot));
-                next();
-                if (j + 2 < n) {
-                    if (!(ok = arrived(slot, phase))) break;
-                    scores(tile, slot);
-                    commit(empty(slot));
-                    next();
+                    for (int c = 4; c < 8; ++c)
+                        mma_ts(d, pt + c * 8, v + c * (2048 >> 4), kIdescV, true);
+                    if (closes) mma_commit(empty(item % kSlots));
                 }
-                commit(s_full(tile));
-            }
-        } else {
-            if ((ok = arrived(slot, phase))) {
-                for (int tile = 0; tile < 2; ++tile) {
-                    scores(tile, slot);
-                    commit(s_full(tile));
+                p_phase ^= 1u << tile;
+                if (more) {
+                    if (opens && !arrived(item + 1)) break;
+                    scores(tile, item + 1);
+                    if (closes && issuer) mma_commit(empty((item + 1) % kSlots));
                 }
-                commit(empty(slot));
-                next();
-            }
-            for (int j = 0; j < n && ok; ++j) {
-                const bool more = j + 1 < n;
-                const int v_slot = slot;
-                const uint32_t v_phase = phase;
-                next();
-                for (int tile = 0; tile < 2; ++tile) {
-                    if (tile == 0 && !(ok = arrived(v_slot, v_phase))) break;
-                    if (!(ok = values(tile, v_slot, j, j > 0))) break;
-                    if (tile == 1) commit(empty(v_slot));
-                    if (more) {
-                        if (tile == 0 && !(ok = arrived(slot, phase))) break;
-                        scores(tile, slot);
-                        if (tile == 1) commit(empty(slot));
-                    }
-                    commit(s_full(tile));
-                }
-                if (more) next();
+                if (issuer) mma_commit(s_full(tile));
+                if (closes) item += more ? 2 : 1;
             }
         }
         // no product may still run when the TMEM is given back
-        commit(drained);
+        if (issuer) mma_commit(drained);
         mbar_drain(drained, 0);
     } else if (warp < 8) {
         // ---- softmax
         asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
         const uint32_t lanes = (uint32_t)(warp & 3) * 32 << 16;
         const uint32_t ts = tmem + lanes + t * 128, to = tmem + lanes + 256 + t * 128;
-        // blocks b0 + first, + step, ...
-        const int first = alone ? t : 0, step = alone ? 2 : 1;
-        const int mine = n > first ? (n - first + step - 1) / step : 0;
-        float m = -INFINITY, l = 0.f;
+        const int first = alone ? t : 0, step = alone ? 2 : 1;  // of the head's blocks
+        uint32_t s_phase = 0;
         bool ok = true;
-        for (int j = 0; j < mine; ++j) {
-            ok = mbar_wait(s_full(t), j & 1, abort_flag);
-            if (!__all_sync(0xFFFFFFFFu, ok)) {
-                ok = false;
-                break;
-            }
-            fence_after();
-            const int64_t left = a.prefix_len - (int64_t)(b0 + first + j * step) * kBlock;
-            uint32_t s[128];
-            float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-            tmem_ld32(ts, s);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                tmem_wait_ld<32>(s + c * 32);
-                if (c < 3) tmem_ld32(ts + (c + 1) * 32, s + (c + 1) * 32);
-                if (left < kBlock) {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (c * 32 + e >= (int)left) s[c * 32 + e] = 0xFF800000u;  // -inf
+        for (int head = head0; head <= head1; ++head) {
+            if (head > head0) load_q(head);
+            mbar_arrive(q_full);
+            const int n = count(head), b0 = first_block(head);
+            const int mine = n > first ? (n - first + step - 1) / step : 0;
+            float m = -INFINITY, l = 0.f;
+            for (int j = 0; j < mine && ok; ++j) {
+                ok = mbar_wait(s_full(t), s_phase, abort_flag);
+                if (!__all_sync(0xFFFFFFFFu, ok)) {
+                    ok = false;
+                    break;
                 }
-#pragma unroll
-                for (int e = 0; e < 32; e += 8)
-#pragma unroll
-                    for (int h = 0; h < 4; ++h)
-                        x[h] = fmaxf(fmaxf(x[h], __uint_as_float(s[c * 32 + e + 2 * h])),
-                                     __uint_as_float(s[c * 32 + e + 2 * h + 1]));
-            }
-            const float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * scale;
-            if (__any_sync(0xFFFFFFFFu, top > m + kRise || m == -INFINITY)) {
-                const float up = fmaxf(m, top);
-                const float f = m == -INFINITY ? 0.f : ex2(m - up);
-                m = up;
-                l *= f;
-                if (j > 0) {  // s_full came after the products on O
-                    uint32_t o[32];
-#pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
-                        tmem_ld32(to + c * 32, o);
-                        tmem_wait_ld<32>(o);
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                        tmem_st32(to + c * 32, o);
-                    }
-                }
-            }
-            const float shift = m == -INFINITY ? 0.f : -m;
-            const uint64_t scale2 = pair(__float_as_uint(scale), __float_as_uint(scale));
-            const uint64_t shift2 = pair(__float_as_uint(shift), __float_as_uint(shift));
-            uint64_t sum[2] = {0ull, 0ull};
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                uint32_t pk[16];
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const uint64_t y = fma2(pair(s[c * 32 + 2 * e], s[c * 32 + 2 * e + 1]), scale2, shift2);
-                    const float p0 = ex2(__uint_as_float((uint32_t)y));
-                    const float p1 = ex2(__uint_as_float((uint32_t)(y >> 32)));
-                    sum[e & 1] = add2(sum[e & 1], pair(__float_as_uint(p0), __float_as_uint(p1)));
-                    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(pk[e]) : "f"(p1), "f"(p0));
-                }
-                tmem_st16(ts + c * 16, pk);
-                if (c & 1) {
-                    tmem_wait_st();
-                    fence_before();
-                    mbar_arrive(c == 1 ? p_half(t) : p_ready(t));
-                }
-            }
-            sum[0] = add2(sum[0], sum[1]);
-            l += __uint_as_float((uint32_t)sum[0]) + __uint_as_float((uint32_t)(sum[0] >> 32));
-        }
-        // every product on O done
-        if (ok && mine > 0) {
-            ok = mbar_wait(s_full(t), mine & 1, abort_flag);
-            fence_after();
-        }
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        if (!ok && lane == 0) atomicOr(&g_prefix_status, HS_ATTN_STATUS_TIMEOUT);
-        if (!ok) m = __int_as_float(0x7FC00000);  // the merge makes such rows NaN
-
-        float4 *xo = reinterpret_cast<float4 *>(smem + kOffRing);
-        float2 *xml = reinterpret_cast<float2 *>(smem + kOffRing + 2 * kTileBytes);
-        const bool sender = alone && t == 1;
-        float f1 = 1.f, f2 = 0.f;
-        if (alone) {
-            // both groups' products are done: nothing reads the ring any more
-            asm volatile("bar.sync 1, 256;" ::: "memory");
-            if (sender) {
-                xml[row] = make_float2(m, mine > 0 ? l : 0.f);
+                s_phase ^= 1;
+                fence_after();
+                const int64_t left = a.prefix_len - (int64_t)(b0 + first + j * step) * kBlock;
+                uint32_t s[128];
+                float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                tmem_ld32(ts, s);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
+                    tmem_wait_ld<32>(s + c * 32);
+                    if (c < 3) tmem_ld32(ts + (c + 1) * 32, s + (c + 1) * 32);
+                    if (left < kBlock) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (c * 32 + e >= (int)left) s[c * 32 + e] = 0xFF800000u;  // -inf
+                    }
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8)
+#pragma unroll
+                        for (int h = 0; h < 4; ++h)
+                            x[h] = fmaxf(fmaxf(x[h], __uint_as_float(s[c * 32 + e + 2 * h])),
+                                         __uint_as_float(s[c * 32 + e + 2 * h + 1]));
+                }
+                const float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * scale;
+                if (__any_sync(0xFFFFFFFFu, top > m + kRise || m == -INFINITY)) {
+                    const float up = fmaxf(m, top);
+                    const float f = m == -INFINITY ? 0.f : ex2(m - up);
+                    m = up;
+                    l *= f;
+                    if (j > 0) {  // s_full came after the products on O
+                        uint32_t o[32];
+#pragma unroll 1
+                        for (int c = 0; c < 4; ++c) {
+                            tmem_ld32(to + c * 32, o);
+                            tmem_wait_ld<32>(o);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                            tmem_st32(to + c * 32, o);
+                        }
+                    }
+                }
+                const float shift = m == -INFINITY ? 0.f : -m;
+                const uint64_t scale2 = pair(__float_as_uint(scale), __float_as_uint(scale));
+                const uint64_t shift2 = pair(__float_as_uint(shift), __float_as_uint(shift));
+                uint64_t sum[2] = {0ull, 0ull};
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const uint64_t y = fma2(pair(s[c * 32 + 2 * e], s[c * 32 + 2 * e + 1]), scale2, shift2);
+                        const float p0 = ex2(__uint_as_float((uint32_t)y));
+                        const float p1 = ex2(__uint_as_float((uint32_t)(y >> 32)));
+                        sum[e & 1] = add2(sum[e & 1], pair(__float_as_uint(p0), __float_as_uint(p1)));
+                        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(pk[e]) : "f"(p1), "f"(p0));
+                    }
+                    tmem_st16(ts + c * 16, pk);
+                    if (c & 1) {
+                        tmem_wait_st();
+                        fence_before();
+                        mbar_arrive(c == 1 ? p_half(t) : p_ready(t));
+                    }
+                }
+                sum[0] = add2(sum[0], sum[1]);
+                l += __uint_as_float((uint32_t)sum[0]) + __uint_as_float((uint32_t)(sum[0] >> 32));
+            }
+            // every product on O done
+            if (ok && mine > 0) {
+                ok = mbar_wait(s_full(t), s_phase, abort_flag);
+                s_phase ^= 1;
+                fence_after();
+            }
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok && lane == 0) atomicOr(&g_prefix_status, HS_ATTN_STATUS_TIMEOUT);
+            if (!ok) m = __int_as_float(0x7FC00000);  // the merge makes such rows NaN
+
+            // the part of (group, head): rows of 512 bytes, one to a thread
+            const int64_t part = (int64_t)(g + head) * n_rows + m_row;
+            float *dst = p.o + part * kDim;
+            asm volatile("" : "+l"(dst));  // computed here, not ahead of the loop over heads
+            if (!alone) {
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
                     uint32_t o[32];
+                    tmem_ld32(to + c * 32, o);
+                    tmem_wait_ld<32>(o);
+                    if (live)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) store32(dst + c * 32 + e * 8, o + e * 8);
+                }
+            } else {
+                // one tile: group t joins both groups' columns [64 t, 64 t + 64)
+                // and hands the others over
+                uint32_t give = s0 + kOffQ + (1 - t) * kTileBytes + row * 16;
+                uint32_t take = s0 + kOffQ + t * kTileBytes + row * 16;
+                asm volatile("" : "+r"(give), "+r"(take));  // as dst
+                float2 *xml = reinterpret_cast<float2 *>(smem + kOffXml);
+                xml[t * kBlock + row] = make_float2(m, l);
+                // both groups' products are done: the queries are not read any more
+                asm volatile("bar.sync 1, 256;" ::: "memory");
+#pragma unroll 1
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t o[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = 0u;
                     if (mine > 0) {
-                        tmem_ld32(to + c * 32, o);
+                        tmem_ld32(to + (1 - t) * 64 + c * 32, o);
                         tmem_wait_ld<32>(o);
                     }
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        xo[(c * 8 + e) * kBlock + row] =
-                            mine > 0 ? make_float4(__uint_as_float(o[4 * e]),
-                                                   __uint_as_float(o[4 * e + 1]),
-                                                   __uint_as_float(o[4 * e + 2]),
-                                                   __uint_as_float(o[4 * e + 3]))
-                                     : make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int e = 0; e < 8; ++e) {
+                        st_shared16(give, o + 4 * e);
+                        give += kBlock * 16;
+                    }
                 }
-            }
-            asm volatile("bar.sync 1, 256;" ::: "memory");
-            if (!sender) {
-                const float2 ml = xml[row];
-                if (ml.x != ml.x) m = ml.x;
-                const float M = m != m ? m : fmaxf(m, ml.x);
+                asm volatile("bar.sync 1, 256;" ::: "memory");
+                const float2 ml = xml[(1 - t) * kBlock + row];
+                const float M = m != m ? m : ml.x != ml.x ? ml.x : fmaxf(m, ml.x);
                 const float base = M == -INFINITY ? 0.f : M;
-                f1 = ex2(m - base);
-                f2 = ex2(ml.x - base);
+                const float f1 = ex2(m - base), f2 = ex2(ml.x - base);
                 l = l * f1 + ml.y * f2;
                 m = M;
-            }
-        }
-        if (!sender) {
-            const int64_t part = ((int64_t)split * a.n_req) * a.q_heads + q_row;
-            float4 *dst = reinterpret_cast<float4 *>(p.o + part * kDim);
+#pragma unroll 1
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t o[32];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                uint32_t o[32];
-                tmem_ld32(to + c * 32, o);
-                tmem_wait_ld<32>(o);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    float4 v = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
-                                           __uint_as_float(o[4 * e + 2]),
-                                           __uint_as_float(o[4 * e + 3]));
-                    if (alone) {
-                        const float4 u = xo[(c * 8 + e) * kBlock + row];
-                        v.x = v.x * f1 + u.x * f2;
-                        v.y = v.y * f1 + u.y * f2;
-                        v.z = v.z * f1 + u.z * f2;
-                        v.w = v.w * f1 + u.w * f2;
+                    for (int e = 0; e < 32; ++e) o[e] = 0u;
+                    if (mine > 0) {
+                        tmem_ld32(to + t * 64 + c * 32, o);
+                        tmem_wait_ld<32>(o);
                     }
-                    if (live) dst[c * 8 + e] = v;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        uint32_t v[4];
+                        ld_shared16(take, v);
+                        take += kBlock * 16;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            o[4 * e + i] = __float_as_uint(__uint_as_float(o[4 * e + i]) * f1 +
+                                                           __uint_as_float(v[i]) * f2);
+                    }
+                    if (live)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            store32(dst + t * 64 + c * 32 + e * 8, o + e * 8);
                 }
             }
-            if (live) p.ml[part] = make_float2(m, l);
+            if ((!alone || t == 0) && live) p.ml[part] = make_float2(m, l);
+            fence_before();  // the next head's products write over S and O
         }
-        fence_before();
     }
     __syncthreads();
     if (warp == 9) {
@@ -662,23 +706,31 @@ EncodeTiled encode_tiled() {
 
 }  // namespace
 
-// Splits of the prefix's key blocks: as many as fill the SMs once with a CTA
-// for every key-value head and pair of row tiles, and at least two blocks
-// each (one for each softmax group).
-PrefixPlan prefix_plan(int n_req, int q_heads, int heads, int64_t prefix_len) {
+// The prefix over at most `ctas` CTAs: as many groups of a CTA for every pair
+// of row tiles as fit (more CTAs than SMs run one behind the other), each at
+// two blocks or more (one for each softmax group).  A multiple of the heads
+// where that costs few groups or the ranges are short: no range then reaches
+// into a second head, which costs its CTA another start and end (about 3 us).
+PrefixPlan prefix_plan(int n_req, int q_heads, int heads, int64_t prefix_len, int ctas) {
     PrefixPlan p = {};
     if (prefix_len < 1) return p;
     const int64_t rows = (int64_t)n_req * (q_heads / heads);
     p.blocks = (int)((prefix_len + kBlock - 1) / kBlock);
     p.row_tiles = (int)((rows + kBlock - 1) / kBlock);
-    const int units = heads * ((p.row_tiles + 1) / 2);
-    int s = kSms / units;
-    if (s > (p.blocks + 1) / 2) s = (p.blocks + 1) / 2;
-    p.splits = s < 1 ? 1 : s;
+    p.total = heads * p.blocks;  // below 2^27
+    const int pairs = (p.row_tiles + 1) / 2;
+    const int most = heads * ((p.blocks + 1) / 2);
+    p.groups = ctas / pairs;
+    if (p.groups > most) p.groups = most;
+    const int whole = p.groups / heads * heads;
+    if (whole > 0 && (whole >= 0.97 * p.groups || p.total < 16 * p.groups)) p.groups = whole;
+    if (p.groups < 1) p.groups = 1;
+    p.lead = (p.groups - 1) / p.blocks;
     return p;
 }
 
-cudaError_t launch_prefix(const GroupArgs &a, const PrefixPlan &p, cudaStream_t st) {
+cudaError_t launch_prefix(const GroupArgs &a, const PrefixPlan &p, const RowsPlan &rows,
+                          cudaStream_t st) {
     const EncodeTiled encode = encode_tiled();
     if (!encode) return cudaErrorNotSupported;
     CUtensorMap map;
@@ -690,11 +742,12 @@ cudaError_t launch_prefix(const GroupArgs &a, const PrefixPlan &p, cudaStream_t 
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return cudaErrorInvalidValue;
-    cudaError_t e = cudaFuncSetAttribute(prefix_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)kSmem);
+    const cudaError_t e = cudaFuncSetAttribute(
+        prefix_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
     if (e != cudaSuccess) return e;
-    const int units = a.heads * ((p.row_tiles + 1) / 2);
-    prefix_kernel<<<(unsigned)units * p.splits, kPrefixThreads, kSmem, st>>>(map, a, p);
+    const int pairs = (p.row_tiles + 1) / 2;
+    prefix_kernel<<<(unsigned)(rows.ctas + p.groups * pairs), kPrefixThreads, kSmem, st>>>(map, a, p,
+                                                                                          rows);
     return cudaGetLastError();
 }
 
