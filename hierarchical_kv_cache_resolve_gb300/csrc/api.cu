@@ -602,7 +602,9 @@ size_t hs_prefix_attention_bytes(int32_t n_req, int32_t q_heads, int32_t heads,
     if (n_req < 1 || n_req > 65535 || !group_layout_ok(q_heads, heads) || prefix_len < 0 ||
         prefix_len > INT32_MAX || k < 0 || k > kMaxRows)
         return 0;
-    return hs::prefix_attention_bytes(n_req, q_heads, heads, prefix_len, k);
+    hs::PrefixPlan pp;
+    hs::RowsPlan p;
+    return hs::prefix_attention_bytes(n_req, q_heads, heads, prefix_len, k, &pp, &p);
 }
 
 int hs_prefix_attention(const void *d_q, const void *d_prefix, int64_t prefix_len,
@@ -616,9 +618,12 @@ int hs_prefix_attention(const void *d_q, const void *d_prefix, int64_t prefix_le
         return HS_ERR_INVALID_ARG;
     if (k > 0 && (!d_cache || !d_idx || cache_rows < 1)) return HS_ERR_INVALID_ARG;
     if (misaligned16(d_cache) || misaligned4(d_idx)) return HS_ERR_INVALID_ARG;
-    const size_t need = hs_prefix_attention_bytes(n_req, q_heads, heads, prefix_len, k);
-    if (need > work_bytes || (need && !d_work)) return HS_ERR_INVALID_ARG;
     if (n_req == 0) return HS_OK;
+    hs::PrefixPlan pp;
+    hs::RowsPlan p;
+    const size_t need =
+        hs::prefix_attention_bytes(n_req, q_heads, heads, prefix_len, k, &pp, &p);
+    if (need > work_bytes || (need && !d_work)) return HS_ERR_INVALID_ARG;
     hs::GroupArgs a = {};
     a.q = static_cast<const uint8_t *>(d_q);
     a.prefix = static_cast<const uint8_t *>(d_prefix);
@@ -632,7 +637,7 @@ int hs_prefix_attention(const void *d_q, const void *d_prefix, int64_t prefix_le
     a.heads = heads;
     a.scale_log2 = scale * 1.4426950408889634f;
     a.out = static_cast<uint8_t *>(d_out);
-    return cuda_ok(hs::launch_prefix_attention(a, d_work, static_cast<cudaStream_t>(stream)))
+    return cuda_ok(hs::launch_prefix_attention(a, pp, p, d_work, static_cast<cudaStream_t>(stream)))
                ? HS_OK
                : HS_ERR_CUDA;
 }

@@ -231,26 +231,35 @@ void share_out(int n_req, int q_heads, int heads, int64_t prefix_len, int k, Pre
     *pp = prefix_plan(n_req, q_heads, heads, prefix_len, kSms);
     *p = rows_plan(n_req, heads, k, kSms);
     if (pp->groups == 0 || p->total == 0) return;
-    double best = INFINITY;
-    PrefixPlan pp_best = {};
-    RowsPlan p_best = {};
-    for (int ctas = 1; ctas < kSms; ++ctas) {
-        const PrefixPlan x = prefix_plan(n_req, q_heads, heads, prefix_len, kSms - ctas);
+    const int pairs = (pp->row_tiles + 1) / 2;
+    // with `ctas` of the SMs for the rows: the plans; the time, and whether it
+    // is the rows'
+    auto split = [&](int ctas, bool *rows_last) {
+        *pp = prefix_plan(n_req, q_heads, heads, prefix_len, kSms - ctas);
         // what the groups leave over goes to the rows
-        const int left = kSms - x.groups * ((x.row_tiles + 1) / 2);
-        const RowsPlan y = rows_plan(n_req, heads, k, left > ctas ? left : ctas);
-        const double waves = (x.groups * ((x.row_tiles + 1) / 2) + y.ctas + kSms - 1) / kSms;
-        const double tx = waves * (13000 + 3000. * ((x.total + x.groups - 1) / x.groups));
-        const double ty = (x.row_tiles > 2 ? 2200. : 3000.) * (double)((y.total + y.ctas * y.subs - 1) / (y.ctas * y.subs));
-        const double t = tx > ty ? tx : ty;
-        if (t < best) {
-            best = t;
-            pp_best = x;
-            p_best = y;
-        }
+        const int left = kSms - pp->groups * pairs;
+        *p = rows_plan(n_req, heads, k, left > ctas ? left : ctas);
+        const int waves = (pp->groups * pairs + p->ctas + kSms - 1) / kSms;
+        const double tx = waves * (13000 + 3000. * ((pp->total + pp->groups - 1) / pp->groups));
+        const int turns = p->ctas * p->subs;
+        const double ty = (pairs > 1 ? 2200. : 3000.) * (double)((p->total + turns - 1) / turns);
+        *rows_last = ty > tx;
+        return tx > ty ? tx : ty;
+    };
+    // more SMs for the rows make them faster and the prefix slower: where the
+    // two meet, or one SM fewer
+    int lo = 1, hi = kSms - 1;
+    bool rows_last;
+    while (lo < hi) {
+        const int mid = (lo + hi) / 2;
+        split(mid, &rows_last);
+        if (rows_last)
+            lo = mid + 1;
+        else
+            hi = mid;
     }
-    *pp = pp_best;
-    *p = p_best;
+    const double at = split(lo, &rows_last);
+    if (lo > 1 && split(lo - 1, &rows_last) >= at) split(lo, &rows_last);
 }
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -321,11 +330,10 @@ cudaError_t launch_merge(const GroupArgs &a, const RowsPlan &p, const PrefixPlan
 
 }  // namespace
 
-size_t prefix_attention_bytes(int n_req, int q_heads, int heads, int64_t prefix_len, int k) {
-    PrefixPlan pp;
-    RowsPlan p;
-    share_out(n_req, q_heads, heads, prefix_len, k, &pp, &p);
-    const size_t n = place_both(&pp, &p, nullptr, n_req, q_heads, heads);
+size_t prefix_attention_bytes(int n_req, int q_heads, int heads, int64_t prefix_len, int k,
+                              PrefixPlan *pp, RowsPlan *p) {
+    share_out(n_req, q_heads, heads, prefix_len, k, pp, p);
+    const size_t n = place_both(pp, p, nullptr, n_req, q_heads, heads);
     return n ? n + kAlignSlack : 0;
 }
 
@@ -336,10 +344,8 @@ size_t attention_weights_bytes(int n_req, int q_heads, int heads, int k) {
            (size_t)n_req * q_heads * k * sizeof(float) + kAlignSlack;
 }
 
-cudaError_t launch_prefix_attention(GroupArgs a, void *work, cudaStream_t st) {
-    PrefixPlan pp;
-    RowsPlan p;
-    share_out(a.n_req, a.q_heads, a.heads, a.prefix_len, a.k, &pp, &p);
+cudaError_t launch_prefix_attention(const GroupArgs &a, PrefixPlan pp, RowsPlan p, void *work,
+                                    cudaStream_t st) {
     place_both(&pp, &p, aligned_work(work), a.n_req, a.q_heads, a.heads);
     cudaError_t e = cudaSuccess;
     if (pp.groups > 0)

@@ -335,9 +335,12 @@ __host__ __device__ inline T range_start(int c, int n, T each, int rest) {
 __host__ __device__ inline int64_t quick_div(int64_t a, int b) {
     return a >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
 }
-size_t prefix_attention_bytes(int n_req, int q_heads, int heads, int64_t prefix_len, int k);
+// the workspace, and the split that launch_prefix_attention is to use
+size_t prefix_attention_bytes(int n_req, int q_heads, int heads, int64_t prefix_len, int k,
+                              PrefixPlan *pp, RowsPlan *p);
 size_t attention_weights_bytes(int n_req, int q_heads, int heads, int k);
-cudaError_t launch_prefix_attention(GroupArgs a, void *work, cudaStream_t st);
+cudaError_t launch_prefix_attention(const GroupArgs &a, PrefixPlan pp, RowsPlan p, void *work,
+                                    cudaStream_t st);
 cudaError_t launch_attention_weights(GroupArgs a, void *work, cudaStream_t st);
 // prefix_attention.cu
 PrefixPlan prefix_plan(int n_req, int q_heads, int heads, int64_t prefix_len, int ctas);

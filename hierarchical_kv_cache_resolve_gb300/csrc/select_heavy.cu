@@ -109,7 +109,7 @@ __device__ __forceinline__ void find_bin(uint32_t *counts, uint32_t need, uint32
 __global__ void __launch_bounds__(kSelThreads)
     select_heavy_kernel(const SelectArgs a, int ctas, int held_max, int list_max) {
     // the weights held, later all candidates' keys [max(held_max, kListMax)];
-    // this CTA's candidates: keys, positions [list_max] each
+    // this CTA's candidates: weights' bits, positions [list_max] each
     extern __shared__ __align__(16) uint32_t dyn[];
     float *vals = reinterpret_cast<float *>(dyn);
     uint32_t *all = dyn;
@@ -234,35 +234,41 @@ __global__ void __launch_bounds__(kSelThreads)
     const uint32_t B = found[0] << 21;
 
     // ---- the candidates: keys above B ----------------------------------------
-    auto list_one = [&](uint32_t key, int j) {
-        const uint32_t e = atomicAdd(&n_list, 1u);
-        if (e < (uint32_t)list_max) {
-            list[e] = key;
-            list_pos[e] = j;
-        }
-    };
-    if (B >= 0x00800000u) {                 // above -infinity: compared as numbers
-        const float fb = __uint_as_float(B & 0x80000000u ? B ^ 0x80000000u : ~B);
-        for (int v0 = 0; v0 < nv; v0 += kEach * kSelThreads) {
-            float4 x[kEach];
-            at(v0 + tid, held, x);
+    // (with B in or below -infinity's bin, all; else compared as numbers)
+    const bool every = B < 0x00800000u;
+    const float fb = __uint_as_float(B & 0x80000000u ? B ^ 0x80000000u : ~B);
+    for (int v0 = 0; v0 < nv; v0 += kEach * kSelThreads) {
+        float4 x[kEach];
+        at(v0 + tid, held, x);
 #pragma unroll
-            for (int u = 0; u < kEach; ++u) {
-                if (!(fmaxf(fmaxf(x[u].x, x[u].y), fmaxf(x[u].z, x[u].w)) > fb)) continue;
-                const int j = 4 * (v0 + u * kSelThreads + tid) - off;
-                if (x[u].x > fb) list_one(order_key(x[u].x), j);
-                if (x[u].y > fb) list_one(order_key(x[u].y), j + 1);
-                if (x[u].z > fb) list_one(order_key(x[u].z), j + 2);
-                if (x[u].w > fb) list_one(order_key(x[u].w), j + 3);
+        for (int u = 0; u < kEach; ++u) {
+            const int j = 4 * (v0 + u * kSelThreads + tid) - off;
+            const float y[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+            uint32_t hit[4], hits = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                hit[e] = every ? j + e >= 0 && j + e < size : y[e] > fb;
+                hits += hit[e];
             }
-        }
-    } else {
-        for (int v0 = 0; v0 < nv; v0 += kEach * kSelThreads) {
-            float4 x[kEach];
-            at(v0 + tid, held, x);
-            each(v0 + tid, x, [&](uint32_t key, int j, bool is) {
-                if (is && key > B) list_one(key, j);
-            });
+            if (!__any_sync(0xFFFFFFFFu, hits)) continue;
+            uint32_t to = hits;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const uint32_t z = __shfl_up_sync(0xFFFFFFFFu, to, d);
+                if (lane >= d) to += z;
+            }
+            uint32_t base = 0;
+            if (lane == 31) base = atomicAdd(&n_list, to);
+            to += __shfl_sync(0xFFFFFFFFu, base, 31) - hits;
+            // (past the list's end its last place is written over: its contents
+            // do not count then)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (hit[e]) {
+                    const uint32_t place = min(to++, (uint32_t)list_max - 1);
+                    list[place] = __float_as_uint(y[e]);
+                    list_pos[place] = j + e;
+                }
         }
     }
     __syncthreads();
@@ -292,7 +298,7 @@ __global__ void __launch_bounds__(kSelThreads)
                 const uint32_t *src = cluster.map_shared_rank(list, c);
                 uint32_t most = 0;
                 for (int j = (warp - c * per) * 32 + lane; j < (int)list_counts[c]; j += per * 32) {
-                    const uint32_t key = src[j];
+                    const uint32_t key = order_key(__uint_as_float(src[j]));
                     all[start + j] = key;
                     most = max(most, key);
                 }
@@ -332,22 +338,25 @@ __global__ void __launch_bounds__(kSelThreads)
             __syncthreads();                // every thread has read what was found
         }
         if (shift > 0) {
-            // at most 32 keys in the bin: every warp ranks them
+            // at most 32 keys in the bin, each ranked by a warp
             for (int j = tid; j < total; j += kSelThreads) {
                 const uint32_t x = all[j];
                 if (x >= base && (x - base) >> shift == 0) few[atomicAdd(&n_few, 1u)] = x;
             }
             __syncthreads();
-            const uint32_t mine = lane < (int)n_few ? few[lane] : 0u;
-            uint32_t above = 0, ahead = 0;
-            for (int s = 0; s < 32; ++s) {
-                const uint32_t y = __shfl_sync(0xFFFFFFFFu, mine, s);
-                above += y > mine;
-                ahead += y == mine && s < lane;
+            if (warp < (int)n_few) {
+                const uint32_t key = lane < (int)n_few ? few[lane] : 0u, mine = few[warp];
+                const uint32_t above = __popc(__ballot_sync(0xFFFFFFFFu, key > mine));
+                const uint32_t ahead =
+                    __popc(__ballot_sync(0xFFFFFFFFu, key == mine) & ((1u << warp) - 1u));
+                if (lane == 0 && above + ahead + 1 == need) {  // one warp
+                    found[0] = mine;
+                    found[1] = need - above;
+                }
             }
-            const int src = __ffs(__ballot_sync(0xFFFFFFFFu, above + ahead + 1 == need)) - 1;
-            T = __shfl_sync(0xFFFFFFFFu, mine, src);
-            need -= __shfl_sync(0xFFFFFFFFu, above, src);
+            __syncthreads();
+            T = found[0];
+            need = found[1];
         } else {
             T = base;
         }
@@ -422,7 +431,8 @@ __global__ void __launch_bounds__(kSelThreads)
             atomicOr((key > T ? gt_bits : eq_bits) + (j >> 5), 1u << (j & 31));
         };
         if (from_list) {
-            for (int j = tid; j < n_mine; j += kSelThreads) mark(list[j], list_pos[j] - w0);
+            for (int j = tid; j < n_mine; j += kSelThreads)
+                mark(order_key(__uint_as_float(list[j])), list_pos[j] - w0);
         } else {
             // the vectors that reach into the window
             for (int v0 = (w0 + off) / 4; 4 * v0 - off < w0 + w1; v0 += kEach * kSelThreads) {
