@@ -21,11 +21,17 @@
 //   warps 0-3 and 4-7  the softmax of tile 0 and 1: a thread per row reads
 //             its 128 scores from TMEM, keeps the running maximum and sum in
 //             registers and writes P back as bf16 over the scores, where the
-//             second product takes it from (its only rounding).
+//             second product takes it from.
 // While one tile's softmax runs, the tensor core works on the other's
 // products.  With a single tile of rows (few queries, bound by HBM) the two
 // softmax groups take every other key block of the same rows, and the two
 // results are joined in shared memory behind the last block of a head.
+//
+// P is rounded once to bf16 (2^-8 of each probability, which averages out over
+// the keys to about the output's own rounding).  A second bf16 term for what
+// the rounding left was measured: it lengthens the chain from one block's
+// scores to the next, 18.7 -> 20.3 us at 57 queries to a head on 20011 keys
+// and 237 -> 284 us at 512 queries on 131072.
 //
 // The maximum only rises when a block exceeds it by more than 2^8: until then
 // P is at most 2^8 too large, which bf16 and the fp32 sums hold as exactly,
@@ -288,6 +294,9 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// kAlone: one tile of rows, whose blocks go to the two groups in turn; else
+// pairs of tiles (the last one's second may be empty).
+template <bool kAlone>
 __global__ void __launch_bounds__(kPrefixThreads, 1)
     prefix_kernel(const __grid_constant__ CUtensorMap map, const GroupArgs a, const PrefixPlan p,
                   const RowsPlan rp) {
@@ -321,8 +330,6 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     const int pair_id = cta % pairs, g = cta / pairs;
     const int group = a.q_heads / a.heads;
     const int n_rows = a.n_req * group;  // at most 65535 * 16
-    // one tile: its blocks go to the two groups in turn
-    const bool alone = 2 * pair_id + 1 == p.row_tiles;
     const int each = p.total / p.groups, rest = p.total % p.groups;
     const int t0 = range_start(g, p.groups, each, rest), t1 = range_start(g + 1, p.groups, each, rest);
     const int head0 = t0 / p.blocks, head1 = (t1 - 1) / p.blocks;
@@ -330,7 +337,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     auto first_block = [&](int head) { return max(0, t0 - head * p.blocks); };
     auto count = [&](int head) { return min(p.blocks, t1 - head * p.blocks) - first_block(head); };
     // how many blocks' keys come before the first block's values
-    auto ahead_of = [&](int n) { return min(alone ? 2 : 1, n); };
+    auto ahead_of = [&](int n) { return min(kAlone ? 2 : 1, n); };
 
     // A head's items of the ring in the order the products use them: K of the
     // first blocks, then V of block j and K of block j + ahead.
@@ -372,32 +379,43 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     }
     // softmax groups: thread = row (TMEM lane) of tile t
     const int t = (warp >> 2) & 1, row = tid & 127;
-    const int m_row = (2 * pair_id + (alone ? 0 : t)) * kBlock + row;
+    const int m_row = (2 * pair_id + (kAlone ? 0 : t)) * kBlock + row;
     const bool live = m_row < n_rows;
     // the queries' sign bits are turned for a negative scale; for scale 0 the
     // queries become 0, so that a masked score stays -inf
     const bool flat = a.scale_log2 == 0.f;
     const float scale = flat ? 1.f : fabsf(a.scale_log2);
     auto load_q = [&](int head) {
-        if (alone && t == 1) return;
+        if (kAlone && t == 1) return;
         const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
         // a warp's 32 rows, two at a time: 16 lanes to a row of 256 bytes
-        const int c = lane & 15;
+        const int c = lane & 15, at0 = (warp & 3) * 32 + (lane >> 4);
+        const int m0 = m_row - row + at0;
+        int r = m0 / group, h = m0 - r * group;  // request and head of the group
         uint8_t *dst = smem + kOffQ + t * kTileBytes + (c >> 3) * kAtom;
+        const uint8_t *src = a.q + (int64_t)head * group * (2 * kDim) + c * 16;
+        uint4 x[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            const int at = (warp & 3) * 32 + 2 * i + (lane >> 4);
-            const int m_at = m_row - row + at;
-            uint4 x = make_uint4(0u, 0u, 0u, 0u);
-            if (m_at < n_rows && !flat) {
-                const int q_row = m_at / group * a.q_heads + head * group + m_at % group;
-                x = __ldg(reinterpret_cast<const uint4 *>(a.q + (int64_t)q_row * (2 * kDim)) + c);
-            }
-            x.x ^= flip;
-            x.y ^= flip;
-            x.z ^= flip;
-            x.w ^= flip;
-            *reinterpret_cast<uint4 *>(dst + at * 128 + (((c & 7) ^ (at & 7)) << 4)) = x;
+            x[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (r < a.n_req && !flat)
+                x[i] = __ldg(reinterpret_cast<const uint4 *>(src + (int64_t)(r * a.q_heads + h) * (2 * kDim)));
+            h += 2;
+#pragma unroll
+            for (int w = 0; w < 2; ++w)
+                if (h >= group) {
+                    h -= group;
+                    ++r;
+                }
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int at = at0 + 2 * i;
+            x[i].x ^= flip;
+            x[i].y ^= flip;
+            x[i].z ^= flip;
+            x[i].w ^= flip;
+            *reinterpret_cast<uint4 *>(dst + at * 128 + (((c & 7) ^ (at & 7)) << 4)) = x[i];
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     };
@@ -441,7 +459,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         };
         // S_t = Q_t K^T, 16 dimensions at a time
         auto scores = [&](int tile, int i) {
-            const uint64_t q = q_op + (alone ? 0 : tile * (kTileBytes >> 4));
+            const uint64_t q = q_op + (kAlone ? 0 : tile * (kTileBytes >> 4));
             const uint64_t k = k_op + i % kSlots * (kTileBytes >> 4);
             if (issuer) {
 #pragma unroll
@@ -457,22 +475,22 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
             fence_after();
             // the first scores of both tiles: of one block, or of two
 #pragma unroll 1
-            for (int tile = 0; tile < (alone ? min(n, 2) : 2) && ok; ++tile) {
-                if ((alone || tile == 0) && !arrived(item)) break;
+            for (int tile = 0; tile < (kAlone ? min(n, 2) : 2) && ok; ++tile) {
+                if ((kAlone || tile == 0) && !arrived(item)) break;
                 scores(tile, item);
                 if (issuer) {
                     mma_commit(s_full(tile));
-                    if (alone || tile == 1) mma_commit(empty(item % kSlots));
+                    if (kAlone || tile == 1) mma_commit(empty(item % kSlots));
                 }
-                if (alone || tile == 1) ++item;
+                if (kAlone || tile == 1) ++item;
             }
             // then the tiles in turn: O_t += P_t V of a block, S_t of the next
-            const int turns = alone ? n : 2 * n;
+            const int turns = kAlone ? n : 2 * n;
 #pragma unroll 1
             for (int u = 0; u < turns && ok; ++u) {
-                const int tile = u & 1, block = alone ? u : u >> 1;
-                const bool opens = alone || tile == 0, closes = alone || tile == 1;
-                const bool more = block + (alone ? 2 : 1) < n;
+                const int tile = u & 1, block = kAlone ? u : u >> 1;
+                const bool opens = kAlone || tile == 0, closes = kAlone || tile == 1;
+                const bool more = block + (kAlone ? 2 : 1) < n;
                 if (opens && !arrived(item)) break;
                 // 16 keys at a time, each half of P as it is ready
                 const uint64_t v = v_op + item % kSlots * (kTileBytes >> 4);
@@ -484,7 +502,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
                         mma_ts(d, pt + c * 8, v + c * (2048 >> 4), kIdescV,
-                               c > 0 || block >= (alone ? 2 : 1));
+                               c > 0 || block >= (kAlone ? 2 : 1));
                 }
                 if (!(ok = mbar_wait(p_ready(tile), ph, abort_flag))) break;
                 fence_after();
@@ -512,7 +530,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
         const uint32_t lanes = (uint32_t)(warp & 3) * 32 << 16;
         const uint32_t ts = tmem + lanes + t * 128, to = tmem + lanes + 256 + t * 128;
-        const int first = alone ? t : 0, step = alone ? 2 : 1;  // of the head's blocks
+        const int first = kAlone ? t : 0, step = kAlone ? 2 : 1;  // of the head's blocks
         uint32_t s_phase = 0;
         bool ok = true;
         for (int head = head0; head <= head1; ++head) {
@@ -607,7 +625,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
             const int64_t part = (int64_t)(g + head) * n_rows + m_row;
             float *dst = p.o + part * kDim;
             asm volatile("" : "+l"(dst));  // computed here, not ahead of the loop over heads
-            if (!alone) {
+            if (!kAlone) {
 #pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
                     uint32_t o[32];
@@ -674,7 +692,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                             store32(dst + t * 64 + c * 32 + e * 8, o + e * 8);
                 }
             }
-            if ((!alone || t == 0) && live) p.ml[part] = make_float2(m, l);
+            if ((!kAlone || t == 0) && live) p.ml[part] = make_float2(m, l);
             fence_before();  // the next head's products write over S and O
         }
     }
@@ -742,12 +760,12 @@ cudaError_t launch_prefix(const GroupArgs &a, const PrefixPlan &p, const RowsPla
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return cudaErrorInvalidValue;
-    const cudaError_t e = cudaFuncSetAttribute(
-        prefix_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    const auto kernel = p.row_tiles == 1 ? prefix_kernel<true> : prefix_kernel<false>;
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
     if (e != cudaSuccess) return e;
     const int pairs = (p.row_tiles + 1) / 2;
-    prefix_kernel<<<(unsigned)(rows.ctas + p.groups * pairs), kPrefixThreads, kSmem, st>>>(map, a, p,
-                                                                                          rows);
+    kernel<<<(unsigned)(rows.ctas + p.groups * pairs), kPrefixThreads, kSmem, st>>>(map, a, p, rows);
     return cudaGetLastError();
 }
 
