@@ -78,6 +78,17 @@ def test_head_layouts(h, group):
     check(s, attend(s))
 
 
+@pytest.mark.parametrize("R,hq,h,P,k", [
+    (48, 8, 1, 5000, 100),      # 384 queries to one head: a pair of tiles and half a pair
+    (100, 32, 8, 1000, 5),      # 400 to each of eight heads
+    (700, 16, 1, 900, 2),       # 11200 queries: 44 pairs of tiles
+    (2500, 128, 8, 300, 1),     # 40000 to each head: more pairs of tiles than SMs
+    (9, 112, 7, 30000, 300)])   # ranges of the prefix that reach into a second head
+def test_many_tiles_and_ranges(R, hq, h, P, k):
+    s = make(R, P, k, hq, h, R + P)
+    check(s, attend(s), requests=sorted({0, 1, R // 3, R // 2, R - 2, R - 1}))
+
+
 def test_a_request_for_every_place_of_a_tile():
     """Groups that do not divide a tile of rows: requests straddle tiles."""
     for hq, R in ((5, 60), (7, 40), (3, 100), (11, 50), (13, 30)):

@@ -106,6 +106,29 @@ def test_keys_that_differ_only_in_their_last_bits():
     assert torch.equal(select(w, None, k, 5).cpu(), want(w, [L], k, 5))
 
 
+@pytest.mark.parametrize("n,L,k", [(1, 131072, 4096), (2, 60000, 3000), (9, 300000, 2500), (80, 9000, 700)])
+def test_heavy_positions_all_in_one_place(n, L, k):
+    """The heaviest positions next to one another: one CTA's share of the
+    candidates holds all of them."""
+    w = torch.linspace(1.0, 0.5, L, device="cuda").repeat(n, 1).contiguous()
+    assert torch.equal(select(w, None, k, 8).cpu(), want(w, [L] * n, k, 8))
+    w = w.flip(1).contiguous()
+    assert torch.equal(select(w, None, k, 8).cpu(), want(w, [L] * n, k, 8))
+
+
+def test_many_equal_weights_at_the_border():
+    """More equal weights than any list holds, on both sides of the border, and
+    long rows of NaN and -infinity."""
+    L, k = 200000, 1500
+    w = torch.full((5, L), 0.5, device="cuda")
+    w[1, ::300] = 0.75                    # 667 above, the rest equal
+    w[2, 1::2] = 0.500001                 # 100000 equal, above 100000 others
+    w[3] = float("nan")
+    w[4] = -float("inf")
+    w[4, ::1000] = -1e30
+    assert torch.equal(select(w, None, k, 16).cpu(), want(w, [L] * 5, k, 16))
+
+
 def test_request_ids():
     w = heavy_tailed(6, 2000, 11)
     ids = [5, 0, -1, 6, 3, 3]
