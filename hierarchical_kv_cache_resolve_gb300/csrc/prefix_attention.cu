@@ -691,6 +691,9 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                         for (int e = 0; e < 4; ++e)
                             store32(dst + t * 64 + c * 32 + e * 8, o + e * 8);
                 }
+                // the next head's queries go where this one's columns were taken
+                // from, and its m and l where these were read
+                if (head < head1) asm volatile("bar.sync 1, 256;" ::: "memory");
             }
             if ((!kAlone || t == 0) && live) p.ml[part] = make_float2(m, l);
             fence_before();  // the next head's products write over S and O

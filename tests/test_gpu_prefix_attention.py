@@ -89,6 +89,18 @@ def test_many_tiles_and_ranges(R, hq, h, P, k):
     check(s, attend(s), requests=sorted({0, 1, R // 3, R // 2, R - 2, R - 1}))
 
 
+@pytest.mark.parametrize("R,hq,P,k", [(9, 56, 50000, 0), (18, 49, 60000, 40), (1, 112, 47001, 3)])
+def test_one_tile_of_queries_and_ranges_into_a_second_head(R, hq, P, k):
+    """Up to 128 queries to each of seven heads, which do not divide the SMs:
+    many ranges of the prefix end in another head than they start in, where the
+    next head's queries take the place of the last one's."""
+    s = make(R, P, k, hq, 7, P)
+    out = attend(s)
+    check(s, out, requests=sorted({0, R // 2, R - 1}))
+    for _ in range(20):
+        assert torch.equal(attend(s).view(torch.int16), out.view(torch.int16))
+
+
 def test_a_request_for_every_place_of_a_tile():
     """Groups that do not divide a tile of rows: requests straddle tiles."""
     for hq, R in ((5, 60), (7, 40), (3, 100), (11, 50), (13, 30)):
