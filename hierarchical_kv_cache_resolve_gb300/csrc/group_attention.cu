@@ -223,9 +223,9 @@ RowsPlan rows_plan(int n_req, int heads, int k, int ctas) {
 
 // How hs_prefix_attention shares the SMs out between the prefix and the
 // requests' own rows: so that both are done at about the same time, by what
-// they were measured to cost (in cycles): a block of 128 keys 3000 for a pair
-// of row tiles, beside 13000 for a CTA's start and end; a tile of 16 rows 2200
-// for each warp, and 3000 where the prefix is bound by HBM too (one pair).
+// they were measured to cost (in cycles): the prefix as its plan says; a tile
+// of 16 rows 2200 for each warp, and 3000 where the prefix is bound by HBM too
+// (one pair).
 void share_out(int n_req, int q_heads, int heads, int64_t prefix_len, int k, PrefixPlan *pp,
                RowsPlan *p) {
     *pp = prefix_plan(n_req, q_heads, heads, prefix_len, kSms);
@@ -240,7 +240,7 @@ void share_out(int n_req, int q_heads, int heads, int64_t prefix_len, int k, Pre
         const int left = kSms - pp->groups * pairs;
         *p = rows_plan(n_req, heads, k, left > ctas ? left : ctas);
         const int waves = (pp->groups * pairs + p->ctas + kSms - 1) / kSms;
-        const double tx = waves * (13000 + 3000. * ((pp->total + pp->groups - 1) / pp->groups));
+        const double tx = waves * pp->cycles;
         const int turns = p->ctas * p->subs;
         const double ty = (pairs > 1 ? 2200. : 3000.) * (double)((p->total + turns - 1) / turns);
         *rows_last = ty > tx;

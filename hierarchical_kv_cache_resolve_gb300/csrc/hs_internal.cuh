@@ -322,6 +322,7 @@ struct PrefixPlan {
     int32_t groups, blocks, row_tiles;
     int32_t total;  // heads * blocks
     int32_t lead;   // (groups - 1) / blocks
+    float cycles;   // what a CTA is expected to take
     float *o;
     float2 *ml;
 };

@@ -8,24 +8,32 @@
 // 4 * 128 * R g flops for 512 bytes: bound by HBM below about R g = 70, by
 // the tensor cores above a few hundred.
 //
-// Work split: the key blocks of 128 of all key-value heads, head after head,
-// are cut into equal contiguous ranges, one for each group of CTAs; the CTAs
-// of a group take the same range (their reads meet in L2) for a pair of row
-// tiles of 128 each.  The first CTAs of the grid take the requests' own rows
-// instead (rows_gather.cuh): the two share the GPU at once, so the rows' reads
-// use the bandwidth that the products leave and neither waits for the other's
-// last CTA.  merge_kernel joins all parts.  One CTA per SM:
-//   warp 8    brings key and value blocks (32 KB each, TMA, 128-byte swizzle)
-//             into a ring of five, in the order the products use them;
-//   warp 9    one thread issues S_t = Q_t K^T and O_t += P_t V;
+// Work split: the key blocks of all key-value heads, head after head, are cut
+// into equal contiguous ranges, one for each group of CTAs; the CTAs of a group
+// take the same range (their reads meet in L2) for a pair of row tiles of 128
+// each.  The first CTAs of the grid take the requests' own rows instead
+// (rows_gather.cuh): the two share the GPU at once, so the rows' reads use the
+// bandwidth that the products leave and neither waits for the other's last CTA.
+// merge_kernel joins all parts.  One CTA per SM:
+//   warp 8    brings key and value blocks (TMA, 128-byte swizzle) into a ring
+//             of 160 KB, in the order the products use them;
+//   warps 9 and 10  one thread issues S_t = Q_t K^T and O_t += P_t V;
 //   warps 0-3 and 4-7  the softmax of tile 0 and 1: a thread per row reads
-//             its 128 scores from TMEM, keeps the running maximum and sum in
+//             its scores from TMEM, keeps the running maximum and sum in
 //             registers and writes P back as bf16 over the scores, where the
 //             second product takes it from.
-// While one tile's softmax runs, the tensor core works on the other's
-// products.  With a single tile of rows (few queries, bound by HBM) the two
-// softmax groups take every other key block of the same rows, and the two
-// results are joined in shared memory behind the last block of a head.
+// Pairs of tiles take blocks of 128 keys, and one warp issues the products of
+// both in turn: while one tile's softmax runs, the tensor core works on the
+// other's products.  (Measured at 512 queries to a head on 131072 keys: 237 us;
+// blocks of 64 keys with their scores in two buffers 280, as products of N = 64
+// read the queries from shared memory twice as often; a warp for each tile
+// 310; sixteen softmax warps, two threads to a row, 250.)
+// With a single tile of rows (few queries, bound by HBM and latency) the two
+// softmax groups take every other block of the same rows, each with a ring and
+// a product warp of its own, and the two results are joined in shared memory
+// behind the last block of a head.  Here blocks of 64 keys in two buffers are
+// the faster ones, as softmax and products of a short range overlap earlier:
+// 8.4 us against 9.7 at 517 keys, 16.8 against 18.8 at 57 queries on 20011.
 //
 // P is rounded once to bf16 (2^-8 of each probability, which averages out over
 // the keys to about the output's own rounding).  A second bf16 term for what
@@ -39,7 +47,8 @@
 // applied as |scale| with the queries' sign turned, so that the row maximum
 // can be taken before scaling.
 //
-// TMEM columns: S_0/P_0 0, S_1/P_1 128, O_0 256, O_1 384.
+// TMEM columns: S_0/P_0 0, S_1/P_1 128 (or two buffers of 64 each), O_0 256,
+// O_1 384.
 //
 // Every wait gives up after a second: the CTA's rows become NaN and
 // HS_ATTN_STATUS_TIMEOUT is set (hs_attention_status); copies and products in
@@ -57,27 +66,30 @@ namespace hs {
 namespace {
 
 constexpr int kDim = 128;
-constexpr int kBlock = 128;                     // keys per block, rows per tile
-constexpr uint32_t kTileBytes = kBlock * kDim * 2;  // 32 KB
-constexpr uint32_t kAtom = kBlock * 128;        // 64 of the 128 dimensions: 16 KB
-constexpr int kSlots = 5;
-constexpr int kPrefixThreads = 384;             // three warpgroups; the last two warps idle
+constexpr int kRows = 128;                      // of a tile of queries
+constexpr uint32_t kTileBytes = kRows * kDim * 2;   // 32 KB of queries
+constexpr uint32_t kAtom = kRows * 128;         // 64 of their 128 dimensions: 16 KB
+constexpr uint32_t kRingBytes = 160 << 10;
+// keys of a block
+__host__ __device__ constexpr int block_keys(bool alone) { return alone ? 64 : 128; }
+constexpr int kPrefixThreads = 384;             // three warpgroups; the last warp idles
 constexpr uint64_t kWaitLimitNs = 1000000000ull;
 constexpr float kRise = 8.f;                    // log2 of how far P may exceed 1
 
 constexpr uint32_t kOffQ = 0;                       // two tiles
 constexpr uint32_t kOffRing = 2 * kTileBytes;
-constexpr uint32_t kOffBar = kOffRing + kSlots * kTileBytes;
-// full[kSlots], empty[kSlots], s_full[2], p_half[2], p_ready[2], q_full, drained
-constexpr int kBars = 2 * kSlots + 8;
+constexpr uint32_t kOffBar = kOffRing + kRingBytes;
+constexpr int kMaxSlots = 10;
+// full[kMaxSlots], empty[kMaxSlots], s_full[2][2], p_ready[2][2], q_full, drained
+constexpr int kBars = 2 * kMaxSlots + 10;
 constexpr uint32_t kOffWord = kOffBar + 8 * kBars;  // TMEM address, abort flag
 // with one tile of rows: both groups' (m, l) [2][128]; half of each group's O
 // goes to the other through the query tiles' places
 constexpr uint32_t kOffXml = kOffWord + 16;
-constexpr uint32_t kSmem = kOffXml + 2 * kBlock * 8;
+constexpr uint32_t kSmem = kOffXml + 2 * kRows * 8;
 static_assert(kSmem <= 232448, "fits an SM");
 static_assert(kOffBar % 8 == 0 && kOffXml % 8 == 0, "barriers and (m, l) are 8-byte aligned");
-static_assert(64 * kBlock * 4 <= kTileBytes, "half of O fits a query tile's place");
+static_assert(64 * kRows * 4 <= kTileBytes, "half of O fits a query tile's place");
 static_assert(rows::kMaxWarps * rows::kWarpSmem <= kSmem, "the row CTAs' rings fit");
 
 __device__ uint32_t g_prefix_status;
@@ -158,10 +170,10 @@ __device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lead) {
            1ull << 46 | 2ull << 61;
 }
 
-// fp32 accumulators, bf16 operands, N = 128, M = 128; bit 16: B is given with
+// fp32 accumulators, bf16 operands, M = 128; bit 16: B is given with
 // its N dimension contiguous
-constexpr uint32_t kIdesc = 1u << 4 | 1u << 7 | 1u << 10 | (128u >> 3) << 17 | (128u >> 4) << 24;
-constexpr uint32_t kIdescV = kIdesc | 1u << 16;
+constexpr uint32_t kIdesc = 1u << 4 | 1u << 7 | 1u << 10 | 128u >> 4 << 24;
+constexpr uint32_t kIdescV = kIdesc | 128u >> 3 << 17 | 1u << 16;  // N = 128
 
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                        bool add) {
@@ -294,8 +306,9 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-// kAlone: one tile of rows, whose blocks go to the two groups in turn; else
-// pairs of tiles (the last one's second may be empty).
+// kAlone: one tile of rows, whose blocks (of 64 keys, their scores in two
+// buffers) go to the two groups in turn; else pairs of tiles (the last one's
+// second may be empty) and blocks of 128 keys.
 template <bool kAlone>
 __global__ void __launch_bounds__(kPrefixThreads, 1)
     prefix_kernel(const __grid_constant__ CUtensorMap map, const GroupArgs a, const PrefixPlan p,
@@ -313,16 +326,25 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         }
         return;
     }
+    constexpr int kKeys = block_keys(kAlone);
+    constexpr uint32_t kItemBytes = kKeys * kDim * 2;  // keys or values of a block
+    constexpr uint32_t kItemAtom = kKeys * 128;        // 64 of their dimensions
+    constexpr int kSlots = kRingBytes / kItemBytes;
+    constexpr uint32_t kIdescS = kIdesc | (uint32_t)kKeys >> 3 << 17;
+    // buffers of scores of a tile, and parts of P whose products are released
+    // one by one: a block of 64 keys each, or the halves of one of 128
+    constexpr int kBufs = kAlone ? 2 : 1, kParts = kAlone ? 1 : 2;
+    static_assert(kSlots <= kMaxSlots && kBufs * kKeys == 128, "ring and TMEM");
     const uint32_t s0 = smem_addr(smem);
     volatile uint32_t *words = reinterpret_cast<volatile uint32_t *>(smem + kOffWord);
     volatile uint32_t *abort_flag = words + 1;
     const uint32_t bars = s0 + kOffBar;
     auto full = [&](int i) { return bars + 8u * i; };
-    auto empty = [&](int i) { return bars + 8u * (kSlots + i); };
-    auto s_full = [&](int t) { return bars + 8u * (2 * kSlots + t); };
-    auto p_half = [&](int t) { return bars + 8u * (2 * kSlots + 2 + t); };
-    auto p_ready = [&](int t) { return bars + 8u * (2 * kSlots + 4 + t); };
-    const uint32_t q_full = bars + 8u * (2 * kSlots + 6), drained = bars + 8u * (2 * kSlots + 7);
+    auto empty = [&](int i) { return bars + 8u * (kMaxSlots + i); };
+    // of tile t and scores buffer b; of tile t and buffer or half b
+    auto s_full = [&](int t, int b) { return bars + 8u * (2 * kMaxSlots + 2 * t + b); };
+    auto p_ready = [&](int t, int b) { return bars + 8u * (2 * kMaxSlots + 4 + 2 * t + b); };
+    const uint32_t q_full = bars + 8u * (2 * kMaxSlots + 8), drained = bars + 8u * (2 * kMaxSlots + 9);
 
     // the CTAs that read the same keys are neighbours
     const int pairs = (p.row_tiles + 1) / 2;
@@ -337,21 +359,32 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     auto first_block = [&](int head) { return max(0, t0 - head * p.blocks); };
     auto count = [&](int head) { return min(p.blocks, t1 - head * p.blocks) - first_block(head); };
     // how many blocks' keys come before the first block's values
-    auto ahead_of = [&](int n) { return min(kAlone ? 2 : 1, n); };
+    auto ahead_of = [&](int n) { return min(kAlone ? 4 : 1, n); };
 
-    // A head's items of the ring in the order the products use them: K of the
-    // first blocks, then V of block j and K of block j + ahead.
-    auto load = [&](int item, int head, int i) {
+    // The ring.  Items come in the order the products use them: for a head, K of
+    // the first blocks, then V of block j and K of block j + ahead.  Pairs of
+    // tiles both use every item; with one tile each group has a ring of its own
+    // for its every other block, so that each ring is waited on in its order.
+    constexpr int kRing = kAlone ? kSlots / 2 : kSlots;
+    int put[2] = {0, 0};                    // items put into each ring (loading thread)
+    auto load = [&](int head, int i) {
         const int n = count(head), ahead = ahead_of(n);
         const int u = i - ahead, both = 2 * (n - ahead);  // both: V, K, V, K, ...; then V only
         const bool is_k = u < 0 || (u < both && (u & 1));
         const int block = u < 0 ? i : u < both ? u / 2 + (u & 1 ? ahead : 0) : u - (n - ahead);
-        const int x = (is_k ? head : a.heads + head) * kDim, slot = item % kSlots;
-        const int y = (first_block(head) + block) * kBlock;
-        const uint32_t dst = s0 + kOffRing + slot * kTileBytes;
-        mbar_expect(full(slot), kTileBytes);
+        const int ring = kAlone ? block & 1 : 0, c = ring ? put[1]++ : put[0]++;
+        const int slot = ring * kRing + c % kRing;
+        if (c >= kRing && !mbar_wait(empty(slot), (c / kRing - 1) & 1, abort_flag)) {
+            ring ? --put[1] : --put[0];
+            return false;
+        }
+        const int x = (is_k ? head : a.heads + head) * kDim;
+        const int y = (first_block(head) + block) * kKeys;
+        const uint32_t dst = s0 + kOffRing + slot * kItemBytes;
+        mbar_expect(full(slot), kItemBytes);
         tma_load(dst, &map, x, y, full(slot));
-        tma_load(dst + kAtom, &map, x + 64, y, full(slot));
+        tma_load(dst + kItemAtom, &map, x + 64, y, full(slot));
+        return true;
     };
     if (warp == 9) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
@@ -364,22 +397,22 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
             mbar_init(full(i), 1);
             mbar_init(empty(i), 1);
         }
-        for (int t = 0; t < 2; ++t) {
-            mbar_init(s_full(t), 1);
-            mbar_init(p_half(t), kBlock);
-            mbar_init(p_ready(t), kBlock);
-        }
-        mbar_init(q_full, 2 * kBlock);
-        mbar_init(drained, 1);
+        for (int t = 0; t < 2; ++t)
+            for (int b = 0; b < 2; ++b) {
+                mbar_init(s_full(t, b), 1);
+                mbar_init(p_ready(t, b), kRows);
+            }
+        mbar_init(q_full, 2 * kRows);
+        mbar_init(drained, kAlone ? 2 : 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         // two items before the queries' loads, which the rest would delay
-        load(0, head0, 0);
-        load(1, head0, 1);
+        load(head0, 0);
+        load(head0, 1);
     }
     // softmax groups: thread = row (TMEM lane) of tile t
     const int t = (warp >> 2) & 1, row = tid & 127;
-    const int m_row = (2 * pair_id + (kAlone ? 0 : t)) * kBlock + row;
+    const int m_row = (2 * pair_id + (kAlone ? 0 : t)) * kRows + row;
     const bool live = m_row < n_rows;
     // the queries' sign bits are turned for a negative scale; for scale 0 the
     // queries become 0, so that a masked score stays -inf
@@ -429,97 +462,141 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     if (warp == 8) {
         // ---- the rest of the ring's items
         if (lane == 0) {
-            int item = 0;
             bool ok = true;
+#pragma unroll 1
             for (int head = head0; head <= head1 && ok; ++head)
-                for (int i = 0, n = 2 * count(head); i < n; ++i, ++item) {
-                    if (head == head0 && i < 2) continue;  // above
-                    if (item >= kSlots &&
-                        !(ok = mbar_wait(empty(item % kSlots), (item / kSlots - 1) & 1, abort_flag)))
-                        break;
-                    load(item, head, i);
-                }
+#pragma unroll 1
+                for (int i = head == head0 ? 2 : 0, n = 2 * count(head); i < n && ok; ++i)
+                    ok = load(head, i);
             // nothing may land after the CTA has left the ring (in a normal run
             // the products have waited for all of it)
-            for (int j = max(0, item - kSlots); j < item; ++j)
-                mbar_drain(full(j % kSlots), (j / kSlots) & 1);
+#pragma unroll 1
+            for (int ring = 0; ring < kSlots / kRing; ++ring)
+#pragma unroll 1
+                for (int c = max(0, put[ring] - kRing); c < put[ring]; ++c)
+                    mbar_drain(full(ring * kRing + c % kRing), (c / kRing) & 1);
         }
-    } else if (warp == 9) {
-        // ---- the products: the whole warp waits, one lane issues
+    } else if (warp == 9 || (kAlone && warp == 10)) {
+        // ---- the products: the whole warp waits, one lane issues.  One warp
+        // for a pair of tiles; with one tile, one for each group's blocks.
+        const int ring = warp - 9;
         const bool issuer = elect_one();
         const uint64_t q_op = operand(s0 + kOffQ, 16);
-        const uint64_t k_op = operand(s0 + kOffRing, 16), v_op = operand(s0 + kOffRing, kAtom);
-        int item = 0;                       // the next item of the ring
-        uint32_t p_phase = 0;               // bit t: of P_t
+        const uint64_t k_op = operand(s0 + kOffRing, 16), v_op = operand(s0 + kOffRing, kItemAtom);
+        uint32_t p_phase = 0;               // bit 2 t + b: of p_ready(t, b)
         bool ok = true;
-        auto arrived = [&](int i) {
-            ok = mbar_wait(full(i % kSlots), (i / kSlots) & 1, abort_flag);
+        // the ring's items one after the other
+        int at = kRing - 1;
+        uint32_t round = 1;                 // its parity
+        auto next_item = [&]() {
+            if (++at == kRing) {
+                at = 0;
+                round ^= 1;
+            }
+            const int slot = ring * kRing + at;
+            ok = mbar_wait(full(slot), round, abort_flag);
             fence_after();
-            return ok;
+            return slot;
         };
-        // S_t = Q_t K^T, 16 dimensions at a time
-        auto scores = [&](int tile, int i) {
+        auto release = [&](int slot) {
+            if (issuer) mma_commit(empty(slot));
+        };
+        // S_t = Q_t K^T into buffer b, 16 dimensions at a time
+        auto scores = [&](int tile, int b, int slot) {
             const uint64_t q = q_op + (kAlone ? 0 : tile * (kTileBytes >> 4));
-            const uint64_t k = k_op + i % kSlots * (kTileBytes >> 4);
+            const uint64_t k = k_op + slot * (kItemBytes >> 4);
             if (issuer) {
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    const uint64_t off = ((c >> 2) * kAtom + (c & 3) * 32) >> 4;
-                    mma_ss(tmem + tile * 128, q + off, k + off, kIdesc, c > 0);
-                }
+                for (int c = 0; c < 8; ++c)
+                    mma_ss(tmem + tile * 128 + b * kKeys, q + (((c >> 2) * kAtom + (c & 3) * 32) >> 4),
+                           k + (((c >> 2) * kItemAtom + (c & 3) * 32) >> 4), kIdescS, c > 0);
             }
         };
+        auto signal = [&](int tile, int b) {
+            if (issuer) mma_commit(s_full(tile, b));
+        };
+        // O_t += P_t V, 16 keys at a time, each part of P as it is ready
+        auto outputs = [&](int tile, int b, int slot, bool first) {
+            const uint64_t v = v_op + slot * (kItemBytes >> 4);
+            const uint32_t pt = tmem + tile * 128 + b * kKeys, d = tmem + 256 + tile * 128;
+#pragma unroll
+            for (int part = 0; part < kParts; ++part) {
+                const int bar = 2 * tile + b + part;
+                if (!(ok = mbar_wait(p_ready(tile, b + part), p_phase >> bar & 1u, abort_flag))) return false;
+                p_phase ^= 1u << bar;
+                fence_after();
+                if (issuer) {
+#pragma unroll
+                    for (int c = 4 * part; c < 4 * part + 4; ++c)
+                        mma_ts(d, pt + c * 8, v + c * (2048 >> 4), kIdescV, c > 0 || !first);
+                }
+            }
+            return true;
+        };
+#pragma unroll 1
         for (int head = head0; head <= head1 && ok; ++head) {
             const int n = count(head);
             ok = mbar_wait(q_full, (head - head0) & 1, abort_flag);
             fence_after();
-            // the first scores of both tiles: of one block, or of two
+            if constexpr (kAlone) {
+                // this group's blocks: every other.  The first scores into both
+                // buffers
+                int b = 0;
 #pragma unroll 1
-            for (int tile = 0; tile < (kAlone ? min(n, 2) : 2) && ok; ++tile) {
-                if ((kAlone || tile == 0) && !arrived(item)) break;
-                scores(tile, item);
-                if (issuer) {
-                    mma_commit(s_full(tile));
-                    if (kAlone || tile == 1) mma_commit(empty(item % kSlots));
+                for (int j = ring; j < min(n, 4); j += 2, ++b) {
+                    const int k = next_item();
+                    if (!ok) break;
+                    scores(ring, b, k);
+                    signal(ring, b);
+                    release(k);
                 }
-                if (kAlone || tile == 1) ++item;
-            }
-            // then the tiles in turn: O_t += P_t V of a block, S_t of the next
-            const int turns = kAlone ? n : 2 * n;
+                // (no block: the softmax group waits for one arrival all the same, so
+                // that it cannot get two heads ahead of this warp)
+                if (ring >= n) signal(ring, 0);
+                // then O += P V of a block, and into the buffer that held its scores
+                // those of the group's block after next
+                b = 0;
 #pragma unroll 1
-            for (int u = 0; u < turns && ok; ++u) {
-                const int tile = u & 1, block = kAlone ? u : u >> 1;
-                const bool opens = kAlone || tile == 0, closes = kAlone || tile == 1;
-                const bool more = block + (kAlone ? 2 : 1) < n;
-                if (opens && !arrived(item)) break;
-                // 16 keys at a time, each half of P as it is ready
-                const uint64_t v = v_op + item % kSlots * (kTileBytes >> 4);
-                const uint32_t pt = tmem + tile * 128, d = tmem + 256 + tile * 128;
-                const uint32_t ph = p_phase >> tile & 1u;
-                if (!(ok = mbar_wait(p_half(tile), ph, abort_flag))) break;
-                fence_after();
-                if (issuer) {
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        mma_ts(d, pt + c * 8, v + c * (2048 >> 4), kIdescV,
-                               c > 0 || block >= (kAlone ? 2 : 1));
+                for (int j = ring; j < n && ok; j += 2, b ^= 1) {
+                    const int v = next_item();
+                    if (!ok || !outputs(ring, b, v, j < 2)) break;
+                    release(v);
+                    if (j + 4 < n) {
+                        const int k = next_item();
+                        if (!ok) break;
+                        scores(ring, b, k);
+                        signal(ring, b);
+                        release(k);
+                    } else {
+                        signal(ring, b);
+                    }
                 }
-                if (!(ok = mbar_wait(p_ready(tile), ph, abort_flag))) break;
-                fence_after();
-                if (issuer) {
-#pragma unroll
-                    for (int c = 4; c < 8; ++c)
-                        mma_ts(d, pt + c * 8, v + c * (2048 >> 4), kIdescV, true);
-                    if (closes) mma_commit(empty(item % kSlots));
+            } else {
+                // the first scores of both tiles; then the tiles in turn: O_t += P_t V
+                // of a block and S_t of the next
+                int k = next_item();
+#pragma unroll 1
+                for (int tile = 0; tile < 2 && ok; ++tile) {
+                    scores(tile, 0, k);
+                    signal(tile, 0);
+                    if (tile == 1) release(k);
                 }
-                p_phase ^= 1u << tile;
-                if (more) {
-                    if (opens && !arrived(item + 1)) break;
-                    scores(tile, item + 1);
-                    if (closes && issuer) mma_commit(empty((item + 1) % kSlots));
+#pragma unroll 1
+                for (int j = 0; j < n && ok; ++j) {
+                    const int v = next_item();
+#pragma unroll 1
+                    for (int tile = 0; tile < 2 && ok; ++tile) {
+                        if (!outputs(tile, 0, v, j == 0)) break;
+                        if (tile == 1) release(v);
+                        if (j + 1 < n) {
+                            if (tile == 0) k = next_item();
+                            if (!ok) break;
+                            scores(tile, 0, k);
+                            if (tile == 1) release(k);
+                        }
+                        signal(tile, 0);
+                    }
                 }
-                if (issuer) mma_commit(s_full(tile));
-                if (closes) item += more ? 2 : 1;
             }
         }
         // no product may still run when the TMEM is given back
@@ -539,23 +616,26 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
             const int n = count(head), b0 = first_block(head);
             const int mine = n > first ? (n - first + step - 1) / step : 0;
             float m = -INFINITY, l = 0.f;
+#pragma unroll 1
             for (int j = 0; j < mine && ok; ++j) {
-                ok = mbar_wait(s_full(t), s_phase, abort_flag);
+                const int buf = j & (kBufs - 1);
+                ok = mbar_wait(s_full(t, buf), s_phase >> buf & 1u, abort_flag);
                 if (!__all_sync(0xFFFFFFFFu, ok)) {
                     ok = false;
                     break;
                 }
-                s_phase ^= 1;
+                s_phase ^= 1u << buf;
                 fence_after();
-                const int64_t left = a.prefix_len - (int64_t)(b0 + first + j * step) * kBlock;
-                uint32_t s[128];
+                const uint32_t tb = ts + buf * kKeys;
+                const int64_t left = a.prefix_len - (int64_t)(b0 + first + j * step) * kKeys;
+                uint32_t s[kKeys];
                 float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                tmem_ld32(ts, s);
+                tmem_ld32(tb, s);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
+                for (int c = 0; c < kKeys / 32; ++c) {
                     tmem_wait_ld<32>(s + c * 32);
-                    if (c < 3) tmem_ld32(ts + (c + 1) * 32, s + (c + 1) * 32);
-                    if (left < kBlock) {
+                    if (c + 1 < kKeys / 32) tmem_ld32(tb + (c + 1) * 32, s + (c + 1) * 32);
+                    if (left < kKeys) {
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
                             if (c * 32 + e >= (int)left) s[c * 32 + e] = 0xFF800000u;  // -inf
@@ -573,7 +653,18 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                     const float f = m == -INFINITY ? 0.f : ex2(m - up);
                     m = up;
                     l *= f;
-                    if (j > 0) {  // s_full came after the products on O
+                    if (j > 0) {
+                        // the products on O so far are done: these scores came
+                        // behind them, or with two buffers those are that the
+                        // other one gets next (waited for again in their turn)
+                        if (kBufs == 2) {
+                            ok = mbar_wait(s_full(t, 1 - buf), s_phase >> (1 - buf) & 1u, abort_flag);
+                            if (!__all_sync(0xFFFFFFFFu, ok)) {
+                                ok = false;
+                                break;
+                            }
+                            fence_after();
+                        }
                         uint32_t o[32];
 #pragma unroll 1
                         for (int c = 0; c < 4; ++c) {
@@ -591,30 +682,32 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                 const uint64_t shift2 = pair(__float_as_uint(shift), __float_as_uint(shift));
                 uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
+                for (int c = 0; c < kKeys / 32; ++c) {
                     uint32_t pk[16];
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
-                        const uint64_t y = fma2(pair(s[c * 32 + 2 * e], s[c * 32 + 2 * e + 1]), scale2, shift2);
+                        const uint64_t y =
+                            fma2(pair(s[c * 32 + 2 * e], s[c * 32 + 2 * e + 1]), scale2, shift2);
                         const float p0 = ex2(__uint_as_float((uint32_t)y));
                         const float p1 = ex2(__uint_as_float((uint32_t)(y >> 32)));
                         sum[e & 1] = add2(sum[e & 1], pair(__float_as_uint(p0), __float_as_uint(p1)));
                         asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(pk[e]) : "f"(p1), "f"(p0));
                     }
-                    tmem_st16(ts + c * 16, pk);
+                    tmem_st16(tb + c * 16, pk);
                     if (c & 1) {
                         tmem_wait_st();
                         fence_before();
-                        mbar_arrive(c == 1 ? p_half(t) : p_ready(t));
+                        mbar_arrive(p_ready(t, kAlone ? buf : c >> 1));
                     }
                 }
                 sum[0] = add2(sum[0], sum[1]);
                 l += __uint_as_float((uint32_t)sum[0]) + __uint_as_float((uint32_t)(sum[0] >> 32));
             }
-            // every product on O done
-            if (ok && mine > 0) {
-                ok = mbar_wait(s_full(t), s_phase, abort_flag);
-                s_phase ^= 1;
+            // every product on O done: the last arrival of each buffer that was used
+#pragma unroll 1
+            for (int buf = 0; buf < max(1, min(mine, kBufs)) && ok; ++buf) {
+                ok = mbar_wait(s_full(t, buf), s_phase >> buf & 1u, abort_flag);
+                s_phase ^= 1u << buf;
                 fence_after();
             }
             ok = __all_sync(0xFFFFFFFFu, ok);
@@ -642,7 +735,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                 uint32_t take = s0 + kOffQ + t * kTileBytes + row * 16;
                 asm volatile("" : "+r"(give), "+r"(take));  // as dst
                 float2 *xml = reinterpret_cast<float2 *>(smem + kOffXml);
-                xml[t * kBlock + row] = make_float2(m, l);
+                xml[t * kRows + row] = make_float2(m, l);
                 // both groups' products are done: the queries are not read any more
                 asm volatile("bar.sync 1, 256;" ::: "memory");
 #pragma unroll 1
@@ -657,11 +750,11 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         st_shared16(give, o + 4 * e);
-                        give += kBlock * 16;
+                        give += kRows * 16;
                     }
                 }
                 asm volatile("bar.sync 1, 256;" ::: "memory");
-                const float2 ml = xml[(1 - t) * kBlock + row];
+                const float2 ml = xml[(1 - t) * kRows + row];
                 const float M = m != m ? m : ml.x != ml.x ? ml.x : fmaxf(m, ml.x);
                 const float base = M == -INFINITY ? 0.f : M;
                 const float f1 = ex2(m - base), f2 = ex2(ml.x - base);
@@ -680,7 +773,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                     for (int e = 0; e < 8; ++e) {
                         uint32_t v[4];
                         ld_shared16(take, v);
-                        take += kBlock * 16;
+                        take += kRows * 16;
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
                             o[4 * e + i] = __float_as_uint(__uint_as_float(o[4 * e + i]) * f1 +
@@ -691,8 +784,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                         for (int e = 0; e < 4; ++e)
                             store32(dst + t * 64 + c * 32 + e * 8, o + e * 8);
                 }
-                // the next head's queries go where this one's columns were taken
-                // from, and its m and l where these were read
+                // the next head's queries go where this one's columns were taken from
                 if (head < head1) asm volatile("bar.sync 1, 256;" ::: "memory");
             }
             if ((!kAlone || t == 0) && live) p.ml[part] = make_float2(m, l);
@@ -730,22 +822,36 @@ EncodeTiled encode_tiled() {
 // The prefix over at most `ctas` CTAs: as many groups of a CTA for every pair
 // of row tiles as fit (more CTAs than SMs run one behind the other), each at
 // two blocks or more (one for each softmax group).  A multiple of the heads
-// where that costs few groups or the ranges are short: no range then reaches
-// into a second head, which costs its CTA another start and end (about 3 us).
+// where the longer ranges cost less than another start and end: no range then
+// reaches into a second head.
 PrefixPlan prefix_plan(int n_req, int q_heads, int heads, int64_t prefix_len, int ctas) {
     PrefixPlan p = {};
     if (prefix_len < 1) return p;
     const int64_t rows = (int64_t)n_req * (q_heads / heads);
-    p.blocks = (int)((prefix_len + kBlock - 1) / kBlock);
-    p.row_tiles = (int)((rows + kBlock - 1) / kBlock);
+    p.row_tiles = (int)((rows + kRows - 1) / kRows);
+    const int keys = block_keys(p.row_tiles == 1);
+    p.blocks = (int)((prefix_len + keys - 1) / keys);
     p.total = heads * p.blocks;  // below 2^27
     const int pairs = (p.row_tiles + 1) / 2;
     const int most = heads * ((p.blocks + 1) / 2);
+    // measured: a CTA's start and end at a head, and 128 keys of a pair of tiles
+    // (with one tile HBM takes as long)
+    // With the whole multiple where it pays: 48.1 -> 43.5 us at 128 queries to
+    // each of 8 heads on 32768 keys, 104 groups instead of 109.
+    auto cycles = [&](int groups) {
+        const int longest = (p.total + groups - 1) / groups;
+        const int heads_more = groups % heads == 0 ? 0 : (longest - 1) / p.blocks + 1;
+        return 13000.f * (1 + heads_more) + 3000.f / 128 * keys * longest;
+    };
     p.groups = ctas / pairs;
     if (p.groups > most) p.groups = most;
-    const int whole = p.groups / heads * heads;
-    if (whole > 0 && (whole >= 0.97 * p.groups || p.total < 16 * p.groups)) p.groups = whole;
     if (p.groups < 1) p.groups = 1;
+    p.cycles = cycles(p.groups);
+    const int whole = p.groups / heads * heads;
+    if (whole > 0 && cycles(whole) <= p.cycles) {
+        p.groups = whole;
+        p.cycles = cycles(whole);
+    }
     p.lead = (p.groups - 1) / p.blocks;
     return p;
 }
@@ -757,7 +863,7 @@ cudaError_t launch_prefix(const GroupArgs &a, const PrefixPlan &p, const RowsPla
     CUtensorMap map;
     const cuuint64_t dims[2] = {(cuuint64_t)a.heads * 2 * kDim, (cuuint64_t)a.prefix_len};
     const cuuint64_t strides[1] = {(cuuint64_t)a.heads * 4 * kDim};
-    const cuuint32_t box[2] = {64, kBlock}, one[2] = {1, 1};
+    const cuuint32_t box[2] = {64, (cuuint32_t)block_keys(p.row_tiles == 1)}, one[2] = {1, 1};
     if (encode(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint8_t *>(a.prefix), dims,
                strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
