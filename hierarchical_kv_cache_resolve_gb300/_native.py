@@ -37,8 +37,8 @@ def nvcc() -> str:
 
 def _inputs():
     files = [os.path.join(CSRC, s) for s in SOURCES]
-    files += [os.path.join(CSRC, "hs_internal.cuh"), os.path.join(CSRC, "rows_gather.cuh"),
-              os.path.join(INCLUDE, "hs.h")]
+    files += [os.path.join(CSRC, h) for h in ("hs_internal.cuh", "barriers.cuh", "rows_gather.cuh")]
+    files += [os.path.join(INCLUDE, "hs.h")]
     return files
 
 

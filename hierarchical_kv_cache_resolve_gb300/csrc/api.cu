@@ -531,10 +531,11 @@ int hs_sparse_attention_heads(const void *d_q, const void *d_cache, int64_t cach
 int hs_attention_status(uint32_t *status) {
     if (!status) return HS_ERR_INVALID_ARG;
     if (!cuda_ok(cudaDeviceSynchronize())) return HS_ERR_CUDA;
-    uint32_t mla = 0, prefix = 0;
-    if (!cuda_ok(hs::attention_status(&mla)) || !cuda_ok(hs::prefix_attention_status(&prefix)))
+    uint32_t mla = 0, prefix = 0, rows = 0;
+    if (!cuda_ok(hs::attention_status(&mla)) || !cuda_ok(hs::prefix_attention_status(&prefix)) ||
+        !cuda_ok(hs::rows_attention_status(&rows)))
         return HS_ERR_CUDA;
-    *status = mla | prefix;
+    *status = mla | prefix | rows;
     return HS_OK;
 }
 

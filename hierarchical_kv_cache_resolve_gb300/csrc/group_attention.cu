@@ -24,12 +24,20 @@ namespace {
 constexpr int kDim = 128;
 constexpr int kMergeThreads = 256;
 
+__device__ uint32_t g_rows_status;
+
 template <bool kScores>
-__global__ void __launch_bounds__(rows::kMaxWarps * 32, 1)
+__global__ void __launch_bounds__(rows::kMaxWarps * 32 + 128, 1)
     rows_kernel(const GroupArgs a, const RowsPlan p) {
     extern __shared__ __align__(128) uint8_t smem[];
+    const int w = (int)threadIdx.x / 32 - a.heads * p.subs;  // from 0: those that bring
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    rows::gather_rows<kScores>(a, p, blockIdx.x, smem);
+    if (w == 0) rows::init(a, smem);
+    __syncthreads();
+    if (w >= 0)
+        rows::bring(a, p, blockIdx.x, smem, w);
+    else
+        rows::attend<kScores>(a, p, blockIdx.x, smem, &g_rows_status);
 }
 
 // The parts of one request and key-value head: those of the prefix, then the
@@ -224,7 +232,7 @@ RowsPlan rows_plan(int n_req, int heads, int k, int ctas) {
 // How hs_prefix_attention shares the SMs out between the prefix and the
 // requests' own rows: so that both are done at about the same time, by what
 // they were measured to cost (in cycles): the prefix as its plan says; a tile
-// of 16 rows 2200 for each warp, and 3000 where the prefix is bound by HBM too
+// of 16 rows 1800 for each warp, and 2600 where the prefix is bound by HBM too
 // (one pair).
 void share_out(int n_req, int q_heads, int heads, int64_t prefix_len, int k, PrefixPlan *pp,
                RowsPlan *p) {
@@ -242,7 +250,7 @@ void share_out(int n_req, int q_heads, int heads, int64_t prefix_len, int k, Pre
         const int waves = (pp->groups * pairs + p->ctas + kSms - 1) / kSms;
         const double tx = waves * pp->cycles;
         const int turns = p->ctas * p->subs;
-        const double ty = (pairs > 1 ? 2200. : 3000.) * (double)((p->total + turns - 1) / turns);
+        const double ty = (pairs > 1 ? 1800. : 2600.) * (double)((p->total + turns - 1) / turns);
         *rows_last = ty > tx;
         return tx > ty ? tx : ty;
     };
@@ -295,10 +303,12 @@ template <bool kScores>
 cudaError_t launch_rows(const GroupArgs &a, const RowsPlan &p, cudaStream_t st) {
     const cudaError_t e = cudaFuncSetAttribute(rows_kernel<kScores>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               rows::kMaxWarps * rows::kWarpSmem);
+                                               rows::kSmem);
     if (e != cudaSuccess) return e;
-    const int warps = a.heads * p.subs;
-    rows_kernel<kScores><<<p.ctas, warps * 32, (size_t)warps * rows::kWarpSmem, st>>>(a, p);
+    const int slots = rows::slots(a.heads, p.subs);
+    const int warps = a.heads * p.subs + rows::bringers(slots);
+    const size_t ring = (size_t)slots * rows::kTile * rows::pitch(a.heads);
+    rows_kernel<kScores><<<p.ctas, warps * 32, rows::kOffSlots + ring, st>>>(a, p);
     return cudaGetLastError();
 }
 
@@ -362,6 +372,19 @@ cudaError_t launch_attention_weights(GroupArgs a, void *work, cudaStream_t st) {
     a.scores = reinterpret_cast<float *>(w + place_both(&none, &p, w, a.n_req, a.q_heads, a.heads));
     const cudaError_t e = launch_rows<true>(a, p, st);
     return e == cudaSuccess ? launch_merge(a, p, none, st) : e;
+}
+
+// Reads the rows kernel's status bits on the current device and clears them.
+cudaError_t rows_attention_status(uint32_t *status) {
+    uint32_t v = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(&v, g_rows_status, sizeof(v));
+    if (e != cudaSuccess) return e;
+    *status = v;
+    if (v) {
+        const uint32_t zero = 0;
+        e = cudaMemcpyToSymbol(g_rows_status, &zero, sizeof(zero));
+    }
+    return e;
 }
 
 }  // namespace hs

@@ -343,6 +343,7 @@ size_t attention_weights_bytes(int n_req, int q_heads, int heads, int k);
 cudaError_t launch_prefix_attention(const GroupArgs &a, PrefixPlan pp, RowsPlan p, void *work,
                                     cudaStream_t st);
 cudaError_t launch_attention_weights(GroupArgs a, void *work, cudaStream_t st);
+cudaError_t rows_attention_status(uint32_t *status);
 // prefix_attention.cu
 PrefixPlan prefix_plan(int n_req, int q_heads, int heads, int64_t prefix_len, int ctas);
 // the prefix's parts, and beside them the rows' (rows.total > 0) on CTAs of their own

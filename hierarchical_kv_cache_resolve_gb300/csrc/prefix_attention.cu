@@ -58,6 +58,7 @@
 
 #include <cuda.h>
 
+#include "barriers.cuh"
 #include "hs.h"
 #include "hs_internal.cuh"
 #include "rows_gather.cuh"
@@ -73,7 +74,6 @@ constexpr uint32_t kRingBytes = 160 << 10;
 // keys of a block
 __host__ __device__ constexpr int block_keys(bool alone) { return alone ? 64 : 128; }
 constexpr int kPrefixThreads = 384;             // three warpgroups; the last warp idles
-constexpr uint64_t kWaitLimitNs = 1000000000ull;
 constexpr float kRise = 8.f;                    // log2 of how far P may exceed 1
 
 constexpr uint32_t kOffQ = 0;                       // two tiles
@@ -90,67 +90,9 @@ constexpr uint32_t kSmem = kOffXml + 2 * kRows * 8;
 static_assert(kSmem <= 232448, "fits an SM");
 static_assert(kOffBar % 8 == 0 && kOffXml % 8 == 0, "barriers and (m, l) are 8-byte aligned");
 static_assert(64 * kRows * 4 <= kTileBytes, "half of O fits a query tile's place");
-static_assert(rows::kMaxWarps * rows::kWarpSmem <= kSmem, "the row CTAs' rings fit");
+static_assert(rows::kSmem <= kSmem, "the row CTAs' rings fit");
 
 __device__ uint32_t g_prefix_status;
-
-__device__ __forceinline__ uint32_t smem_addr(const void *p) {
-    return (uint32_t)__cvta_generic_to_shared(p);
-}
-
-__device__ __forceinline__ uint64_t globaltimer() {
-    uint64_t t;
-    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-    return t;
-}
-
-__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
-}
-
-__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-
-__device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
-                 : "memory");
-}
-
-__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-
-// Waits for the phase of `bar` with this parity; false after the limit, or
-// once another wait of the CTA has given up.
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity,
-                                          volatile uint32_t *abort_flag) {
-    if (mbar_try(bar, parity)) return true;
-    const uint64_t t0 = globaltimer();
-    while (!mbar_try(bar, parity)) {
-        if (*abort_flag || globaltimer() - t0 > kWaitLimitNs) {
-            *abort_flag = 1;
-            return false;
-        }
-    }
-    return true;
-}
-
-// The same without regard to the flag: what must have ended before the CTA
-// may reuse or leave its memory.
-__device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity) {
-    const uint64_t t0 = globaltimer();
-    while (!mbar_try(bar, parity) && globaltimer() - t0 <= kWaitLimitNs) {
-    }
-}
 
 __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *map, int x, int y,
                                          uint32_t bar) {
@@ -318,11 +260,15 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);  // known to be the same in a warp
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if ((int)blockIdx.x < rp.ctas) {  // (0 without own rows)
+        if (warp == 8) rows::init(a, smem);
+        __syncthreads();
         if (warp >= 8) {
             asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+            rows::bring(a, rp, blockIdx.x, smem, warp - 8);
         } else {
             asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
-            if (warp < a.heads * rp.subs) rows::gather_rows<false>(a, rp, blockIdx.x, smem);
+            if (warp < a.heads * rp.subs)
+                rows::attend<false>(a, rp, blockIdx.x, smem, &g_prefix_status);
         }
         return;
     }
@@ -404,8 +350,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
             }
         mbar_init(q_full, 2 * kRows);
         mbar_init(drained, kAlone ? 2 : 1);
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        mbar_init_done();
         // two items before the queries' loads, which the rest would delay
         load(head0, 0);
         load(head0, 1);
