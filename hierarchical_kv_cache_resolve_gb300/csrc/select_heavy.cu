@@ -15,13 +15,20 @@
 //   the candidates: all keys above B, a little more than are wanted, listed
 //     with their positions.  If they are fewer, T = B (many equal weights:
 //     zeros, above all);
-//   T among the candidates, whose keys every CTA copies from all lists: counts
-//     in 2048 bins over their own range, and again within the bin found until
-//     it holds no more keys than a warp can rank.
-// So all weights are only compared with B, once; and the CTAs wait for one
+//   T among the candidates, whose keys every CTA writes into all others' shared
+//     memory: counts in 2048 bins over their own range, and again within the bin
+//     found until it holds no more keys than a warp can rank.
+// So all weights are only compared with B, once, and those of a warp's 128
+// neighbours not even that where their maximum is no larger (three in four
+// with 2048 of a million wanted); and the CTAs wait for one
 // another twice, once for the maxima's counts and once for the lists.  With
 // more candidates than the lists hold (a large k) every CTA counts all its
 // keys instead, by 11, 11 and 10 bits.
+// Measured: 11.2 us for 32 requests of 32768 positions (clusters of 4; about
+// ten steps of 0.5 to 1.3 us), 24.3 us for 8 of 2^20 (clusters of 12, 33.5 MB
+// read in 7 us).  Listed candidates copied by the CTAs from one another, not
+// written by their finders, which leaves memory to be kept until the others are
+// done: 12.0 us; every weight compared: 26.4.
 // The kept positions -- keys above T, and the first of those equal to it --
 // are marked in two bitmaps over the CTA's range, whose prefix sums give each
 // its place in ascending order.
@@ -42,15 +49,14 @@ constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kSelCluster = 16;
-constexpr int kListMax = 8192;        // candidates of the whole cluster
+constexpr int kListMax = 8192;        // candidates of a CTA
+constexpr int kAllMax = 2 * kListMax; // of the whole cluster, in equal shares
 constexpr int kMinChunk = 2048;       // positions per CTA worth splitting for
-// Weights and candidates that a CTA keeps in shared memory, candidates of a
-// CTA in a small cluster and in one of eight or more
-constexpr int kHeldMax = 36864, kHeldMaxWide = 49152;
-constexpr int kListWide = 2048;
+constexpr int kDynMax = (232448 - 17408) / 4;  // words of shared memory beside the static arrays
 constexpr int kWindow = kBins * 32;   // positions the bitmaps hold
-static_assert((kHeldMax + 2 * kListMax) * 4 + 17408 <= 232448, "beside the static arrays");
-static_assert((kHeldMaxWide + 2 * kListWide) * 4 + 17408 <= 232448, "beside the static arrays");
+constexpr int kWords = 4;             // of a bitmap, to a thread, where memory is left over
+static_assert(32 * 32 * kWords < 1 << 16, "two counts in a word");
+static_assert(kDynMax > kAllMax + kListMax + kMinChunk, "room for weights");
 
 // Unsigned order of the keys = order of the weights; -0 counts as 0, NaN as
 // -infinity.
@@ -60,6 +66,13 @@ __device__ __forceinline__ uint32_t order_key(float w) {
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 constexpr uint32_t kZeroKey = 0x80000000u;
+
+// The largest of a warp's values; NaN counts as nothing.
+__device__ __forceinline__ float warp_max(float x) {
+    float y;
+    asm("redux.sync.max.f32 %0, %1, 0xFFFFFFFF;" : "=f"(y) : "f"(x));
+    return y;
+}
 
 // Counts this warp's keys by `bin` where `active`.
 __device__ __forceinline__ void count(uint32_t *hist, uint32_t key, int shift, uint32_t mask,
@@ -108,22 +121,22 @@ __device__ __forceinline__ void find_bin(uint32_t *counts, uint32_t need, uint32
 
 __global__ void __launch_bounds__(kSelThreads)
     select_heavy_kernel(const SelectArgs a, int ctas, int held_max, int list_max) {
-    // the weights held, later all candidates' keys [max(held_max, kListMax)];
-    // this CTA's candidates: weights' bits, positions [list_max] each
+    // the weights held [held_max]; the candidates' keys of every CTA, and the
+    // positions of this one's [list_max each]
     extern __shared__ __align__(16) uint32_t dyn[];
     float *vals = reinterpret_cast<float *>(dyn);
-    uint32_t *all = dyn;
-    uint32_t *list = dyn + max(held_max, kListMax);
-    int32_t *list_pos = reinterpret_cast<int32_t *>(list + list_max);
+    uint32_t *all = dyn + held_max;
+    int32_t *list_pos = reinterpret_cast<int32_t *>(all + ctas * list_max);
     // this CTA's counts and the cluster's, zero between uses; in the end the
     // bitmaps of the keys above T and equal to it
     __shared__ uint32_t hist[kBins], sums[kBins];
     __shared__ uint32_t warp_a[kSelWarps], warp_b[kSelWarps], few[32], ahead_b[kSelWarps];
-    __shared__ uint32_t found[3], highest, n_few, n_list;
-    __shared__ uint32_t totals[2][kSelCluster], list_counts[kSelCluster];
+    __shared__ uint32_t found[3], n_few, n_list, my_top;
+    __shared__ uint32_t totals[2][kSelCluster], list_counts[kSelCluster], tops[kSelCluster];
     cg::cluster_group cluster = cg::this_cluster();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int i = blockIdx.x / ctas, rank = blockIdx.x % ctas;
+    uint32_t *list = all + rank * list_max;
     int32_t *out = a.sel + (int64_t)i * a.k;
     const int32_t req = a.req_ids ? a.req_ids[i] : i;
     if (req < 0 || req >= a.weight_rows) {  // the whole cluster alike
@@ -153,13 +166,15 @@ __global__ void __launch_bounds__(kSelThreads)
     const int nv = (off + size + 3) / 4;
     const int held = min(nv, held_max / 4);
     // Vectors v, v + 1024, ..., kEach of them: those below `from` out of shared
-    // memory, the others with their global loads issued together.
+    // memory, the others with their global loads issued together; with bit u of
+    // `rows` clear, x[u] is left.
     constexpr int kEach = 4;
-    auto at = [&](int v, int from, float4 *x) {
+    auto at = [&](int v, int from, float4 *x, uint32_t rows = 0xFu) {
 #pragma unroll
         for (int u = 0; u < kEach; ++u) {
             const int t = v + u * kSelThreads, j = 4 * t - off;
-            if (t < from) {
+            if (!(rows >> u & 1u)) {
+            } else if (t < from) {
                 x[u] = reinterpret_cast<const float4 *>(vals)[t];
             } else if (j >= 0 && j + 3 < size) {
                 x[u] = __ldg(reinterpret_cast<const float4 *>(wc + j));
@@ -185,8 +200,9 @@ __global__ void __launch_bounds__(kSelThreads)
 
     // ---- read; the maxima's leading bits ------------------------------------
     for (int b = tid; b < kBins; b += kSelThreads) hist[b] = sums[b] = 0;
-    if (tid == 0) found[0] = highest = n_list = 0;
+    if (tid == 0) found[0] = my_top = n_list = 0;
     float4 top = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+    float row_top = -INFINITY;   // of the warp's rows of 32 vectors lane, lane + 32, ...
     for (int v0 = 0; v0 < nv; v0 += kEach * kSelThreads) {
         float4 x[kEach];
         at(v0 + tid, 0, x);
@@ -198,10 +214,14 @@ __global__ void __launch_bounds__(kSelThreads)
             top.y = fmaxf(top.y, x[u].y);
             top.z = fmaxf(top.z, x[u].z);
             top.w = fmaxf(top.w, x[u].w);
+            const float row = warp_max(fmaxf(fmaxf(x[u].x, x[u].y), fmaxf(x[u].z, x[u].w)));
+            if (lane == (v0 / kSelThreads + u) % 32) row_top = fmaxf(row_top, row);
         }
     }
     __syncthreads();
     cluster.barrier_arrive();               // this CTA's sums are zero
+    const float warp_top = warp_max(row_top);
+    if (lane == 0) atomicMax(&my_top, order_key(warp_top));
     // as few groups as are half as many again as the positions wanted
     const uint32_t groups = (uint32_t)ctas * kSelThreads;
     if (2 * groups >= 3 * want) {
@@ -237,11 +257,16 @@ __global__ void __launch_bounds__(kSelThreads)
     // (with B in or below -infinity's bin, all; else compared as numbers)
     const bool every = B < 0x00800000u;
     const float fb = __uint_as_float(B & 0x80000000u ? B ^ 0x80000000u : ~B);
+    // the warp's rows that have any
+    const uint32_t rows = __ballot_sync(0xFFFFFFFFu, every || row_top > fb);
     for (int v0 = 0; v0 < nv; v0 += kEach * kSelThreads) {
+        const uint32_t here = rows >> v0 / kSelThreads % 32;  // kEach divides 32
+        if (!(here & ((1u << kEach) - 1u))) continue;
         float4 x[kEach];
-        at(v0 + tid, held, x);
+        at(v0 + tid, held, x, here);
 #pragma unroll
         for (int u = 0; u < kEach; ++u) {
+            if (!(here >> u & 1u)) continue;
             const int j = 4 * (v0 + u * kSelThreads + tid) - off;
             const float y[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
             uint32_t hit[4], hits = 0;
@@ -266,58 +291,51 @@ __global__ void __launch_bounds__(kSelThreads)
             for (int e = 0; e < 4; ++e)
                 if (hit[e]) {
                     const uint32_t place = min(to++, (uint32_t)list_max - 1);
-                    list[place] = __float_as_uint(y[e]);
+                    list[place] = order_key(y[e]);
                     list_pos[place] = j + e;
                 }
         }
     }
     __syncthreads();
-    if (tid < ctas) cluster.map_shared_rank(list_counts, tid)[rank] = n_list;
+    // warps share the CTAs out: where to write, later whose keys to look at
+    const int per = kSelWarps / ctas, other = warp / per, first = (warp - other * per) * 32;
+    if (other < ctas && other != rank && n_list <= (uint32_t)list_max) {
+        uint32_t *dst = cluster.map_shared_rank(list, other);
+        for (int j = first + lane; j < (int)n_list; j += per * 32) dst[j] = list[j];
+    }
+    if (tid < ctas) {
+        cluster.map_shared_rank(list_counts, tid)[rank] = n_list;
+        cluster.map_shared_rank(tops, tid)[rank] = my_top;
+    }
     cluster.sync();
     uint64_t candidates = 0;
+    uint32_t highest = 0;
     bool listed = true;                     // the lists hold all candidates
     for (int c = 0; c < ctas; ++c) {
         candidates += list_counts[c];
+        highest = max(highest, tops[c]);
         listed &= list_counts[c] <= (uint32_t)list_max;
     }
-    listed &= candidates <= kListMax;
     const bool from_list = candidates >= want && listed;
+    // a longer range's bitmaps where the weights were, in one window
+    const bool roomy = from_list && size > kWindow && held_max >= 2 * kWords * kSelThreads;
 
     uint32_t T = B, need = want - (uint32_t)candidates;
     uint32_t gt0 = 0, eq0 = 0;              // kept and equal ones before this CTA's
     if (from_list) {
-        // every CTA's candidates, in the order of the ranges: warps share the
-        // lists out
-        const int total = (int)candidates;
-        int before = 0;                     // candidates of lower ranges
-        {
-            const int per = kSelWarps / ctas, c = warp / per;
-            if (c < ctas) {
-                int start = 0;
-                for (int t = 0; t < c; ++t) start += (int)list_counts[t];
-                const uint32_t *src = cluster.map_shared_rank(list, c);
-                uint32_t most = 0;
-                for (int j = (warp - c * per) * 32 + lane; j < (int)list_counts[c]; j += per * 32) {
-                    const uint32_t key = order_key(__uint_as_float(src[j]));
-                    all[start + j] = key;
-                    most = max(most, key);
-                }
-                most = __reduce_max_sync(0xFFFFFFFFu, most);
-                if (lane == 0) atomicMax(&highest, most);
-            }
-            for (int t = 0; t < rank; ++t) before += (int)list_counts[t];
-        }
-        __syncthreads();
-        cluster.barrier_arrive();           // the other CTAs' lists are read
+        if (roomy)
+            for (int b = tid; b < 2 * kWords * kSelThreads; b += kSelThreads) dyn[b] = 0;
+        const int total = other < ctas ? (int)list_counts[other] : 0;
+        const uint32_t *keys = all + min(other, ctas - 1) * list_max;
         // the need-th largest lies in [base, base + 2048 << shift)
         uint32_t base = B;
         need = want;
         int shift = max(0, 32 - __clz(highest - B) - 11);
         while (true) {
-            for (int j0 = 0; j0 < total; j0 += kSelThreads) {
-                const uint32_t x = j0 + tid < total ? all[j0 + tid] : 0u;
+            for (int j0 = first; j0 < total; j0 += per * 32) {
+                const uint32_t x = j0 + lane < total ? keys[j0 + lane] : 0u;
                 const uint32_t bin = (x - base) >> shift;
-                const bool in = j0 + tid < total && x >= base && bin < kBins;
+                const bool in = j0 + lane < total && x >= base && bin < kBins;
                 const uint32_t some = __ballot_sync(0xFFFFFFFFu, in);
                 if (!some) continue;
                 // many equal keys: the first lane's bin in one addition
@@ -339,8 +357,8 @@ __global__ void __launch_bounds__(kSelThreads)
         }
         if (shift > 0) {
             // at most 32 keys in the bin, each ranked by a warp
-            for (int j = tid; j < total; j += kSelThreads) {
-                const uint32_t x = all[j];
+            for (int j = first + lane; j < total; j += per * 32) {
+                const uint32_t x = keys[j];
                 if (x >= base && (x - base) >> shift == 0) few[atomicAdd(&n_few, 1u)] = x;
             }
             __syncthreads();
@@ -360,10 +378,11 @@ __global__ void __launch_bounds__(kSelThreads)
         } else {
             T = base;
         }
-        for (int j = tid; j < before; j += kSelThreads) {
-            gt0 += all[j] > T;
-            eq0 += all[j] == T;
-        }
+        if (other < rank)
+            for (int j = first + lane; j < total; j += per * 32) {
+                gt0 += keys[j] > T;
+                eq0 += keys[j] == T;
+            }
     } else {
         if (candidates >= want) {
             uint32_t prefix = 0;
@@ -422,17 +441,19 @@ __global__ void __launch_bounds__(kSelThreads)
     // (the sums over the threads are taken with the first window's)
 
     // ---- marked and written in order -----------------------------------------
-    uint32_t *gt_bits = hist, *eq_bits = sums;
+    uint32_t *gt_bits = roomy ? dyn : hist;
+    uint32_t *eq_bits = roomy ? gt_bits + kWords * kSelThreads : sums;
+    const int window = roomy ? kWords * kSelThreads * 32 : kWindow;
     const int n_mine = from_list ? (int)list_counts[rank] : 0;
-    for (int w0 = 0; w0 < size || w0 == 0; w0 += kWindow) {
-        const int w1 = min(size - w0, kWindow);  // positions w0 + [0, w1)
+    for (int w0 = 0; w0 < size || w0 == 0; w0 += window) {
+        const int w1 = min(size - w0, window);  // positions w0 + [0, w1)
         auto mark = [&](uint32_t key, int j) {
             if (key < T || j < 0 || j >= w1) return;
             atomicOr((key > T ? gt_bits : eq_bits) + (j >> 5), 1u << (j & 31));
         };
         if (from_list) {
             for (int j = tid; j < n_mine; j += kSelThreads)
-                mark(order_key(__uint_as_float(list[j])), list_pos[j] - w0);
+                mark(list[j], list_pos[j] - w0);
         } else {
             // the vectors that reach into the window
             for (int v0 = (w0 + off) / 4; 4 * v0 - off < w0 + w1; v0 += kEach * kSelThreads) {
@@ -446,66 +467,72 @@ __global__ void __launch_bounds__(kSelThreads)
         const uint32_t g0 = __reduce_add_sync(0xFFFFFFFFu, gt0);
         const uint32_t q0 = __reduce_add_sync(0xFFFFFFFFu, eq0);
         __syncthreads();
-        // a thread writes one or two consecutive words
-        const int words = (w1 + 31) / 32, each_words = words > kSelThreads ? 2 : 1;
-        uint32_t g[2] = {0u, 0u}, q[2] = {0u, 0u};
+        // a thread writes a few consecutive words
+        const int words = (w1 + 31) / 32;
+        const int each_words = words <= kSelThreads / 4 ? 1 : words <= kSelThreads / 2 ? 2 : kWords;
+        const bool busy = warp * 32 * each_words < words, last = w0 + window >= size;
+        uint32_t g[kWords] = {}, q[kWords] = {};
+        uint32_t ng = 0, nq = 0, incl = 0;  // this thread's; up to it (equal ones << 16)
+        if (busy) {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int b = each_words * tid + e;
-            if (e < each_words && b < words) {
-                g[e] = gt_bits[b];
-                q[e] = eq_bits[b];
-                gt_bits[b] = eq_bits[b] = 0;
+            for (int e = 0; e < kWords; ++e) {
+                const int b = each_words * tid + e;
+                if (e < each_words && b < words) {
+                    g[e] = gt_bits[b];
+                    q[e] = eq_bits[b];
+                    if (!last) gt_bits[b] = eq_bits[b] = 0;
+                }
+                ng += __popc(g[e]);
+                nq += __popc(q[e]);
             }
-        }
-        const uint32_t ng = __popc(g[0]) + __popc(g[1]), nq = __popc(q[0]) + __popc(q[1]);
-        uint32_t ig = ng, iq = nq;
+            incl = ng | nq << 16;           // a warp has at most 32 * 32 * kWords
 #pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const uint32_t yg = __shfl_up_sync(0xFFFFFFFFu, ig, d);
-            const uint32_t yq = __shfl_up_sync(0xFFFFFFFFu, iq, d);
-            if (lane >= d) {
-                ig += yg;
-                iq += yq;
+            for (int d = 1; d < 32; d <<= 1) {
+                const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+                if (lane >= d) incl += y;
             }
         }
         // a warp's words, and what its threads had before the window
         if (lane == 31) {
-            warp_a[warp] = ig;
-            warp_b[warp] = iq;
+            warp_a[warp] = incl & 0xFFFFu;
+            warp_b[warp] = incl >> 16;
         }
         if (lane == 0) {
             few[warp] = g0;
             ahead_b[warp] = q0;
         }
         __syncthreads();
-        const uint32_t wg = warp_a[lane], wq = warp_b[lane];
-        gt0 = __reduce_add_sync(0xFFFFFFFFu, few[lane]);
-        eq0 = __reduce_add_sync(0xFFFFFFFFu, ahead_b[lane]);
-        uint32_t pg = gt0 + ig - ng + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? wg : 0u);
-        uint32_t pq = eq0 + iq - nq + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? wq : 0u);
-        // carried on by one thread
-        const uint32_t next_g = gt0 + __reduce_add_sync(0xFFFFFFFFu, wg);
-        const uint32_t next_q = eq0 + __reduce_add_sync(0xFFFFFFFFu, wq);
-        gt0 = tid == 0 ? next_g : 0u;
-        eq0 = tid == 0 ? next_q : 0u;
+        if (busy || !last) {
+            const uint32_t wg = warp_a[lane], wq = warp_b[lane];
+            gt0 = __reduce_add_sync(0xFFFFFFFFu, few[lane]);
+            eq0 = __reduce_add_sync(0xFFFFFFFFu, ahead_b[lane]);
+            uint32_t pg = gt0 + (incl & 0xFFFFu) - ng +
+                          __reduce_add_sync(0xFFFFFFFFu, lane < warp ? wg : 0u);
+            uint32_t pq = eq0 + (incl >> 16) - nq +
+                          __reduce_add_sync(0xFFFFFFFFu, lane < warp ? wq : 0u);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            uint32_t any = g[e] | q[e];
-            while (any) {
-                const int b = __ffs(any) - 1;
-                any &= any - 1;
-                const bool above = g[e] >> b & 1u;
-                if (above || pq < need)
-                    out[pg + min(pq, need)] =
-                        (int32_t)(lo + w0 + (each_words * tid + e) * 32 + b);
-                pg += above;
-                pq += !above;
+            for (int e = 0; e < kWords; ++e) {
+                uint32_t any = g[e] | q[e];
+                while (any) {
+                    const int b = __ffs(any) - 1;
+                    any &= any - 1;
+                    const bool above = g[e] >> b & 1u;
+                    if (above || pq < need)
+                        out[pg + min(pq, need)] =
+                            (int32_t)(lo + w0 + (each_words * tid + e) * 32 + b);
+                    pg += above;
+                    pq += !above;
+                }
             }
+            // carried on by one thread
+            const uint32_t next_g = gt0 + __reduce_add_sync(0xFFFFFFFFu, wg);
+            const uint32_t next_q = eq0 + __reduce_add_sync(0xFFFFFFFFu, wq);
+            gt0 = tid == 0 ? next_g : 0u;
+            eq0 = tid == 0 ? next_q : 0u;
         }
-        __syncthreads();                    // the window's words and sums are read
+        if (!last) __syncthreads();         // the window's words and sums are read
     }
-    cluster.barrier_wait();
+    if (!from_list) cluster.barrier_wait();
 }
 
 }  // namespace
@@ -529,14 +556,14 @@ cudaError_t launch_select_heavy(const SelectArgs &a, int n_req, cudaStream_t st)
     // a range's positions fit 31 bits with room for a step of the loops
     while (a.n_positions > (int64_t)ctas << 30) ctas *= 2;
     // a range's weights start at any of the four words of a vector
-    const bool wide = ctas >= 8;
-    const int most = wide ? kHeldMaxWide : kHeldMax, list_max = wide ? kListWide : kListMax;
+    const int list_max = kAllMax / ctas < kListMax ? kAllMax / ctas : kListMax;
+    const int most = (kDynMax - (ctas + 1) * list_max) / 4 * 4;
     const int64_t chunk = (a.n_positions + ctas - 1) / ctas + 3;
     const int held_max = (int)(chunk < most ? (chunk + 3) / 4 * 4 : most);
-    const size_t smem = ((size_t)(held_max > kListMax ? held_max : kListMax) + 2 * list_max) * 4;
+    const size_t smem = ((size_t)held_max + (ctas + 1) * list_max) * 4;
     cudaError_t e = cudaFuncSetAttribute(select_heavy_kernel,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         232448 - 17408);
+                                         kDynMax * 4);
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(select_heavy_kernel,
                                  cudaFuncAttributeNonPortableClusterSizeAllowed, 1);

@@ -116,6 +116,17 @@ def test_heavy_positions_all_in_one_place(n, L, k):
     assert torch.equal(select(w, None, k, 8).cpu(), want(w, [L] * n, k, 8))
 
 
+@pytest.mark.parametrize("n,L,k", [(80, 200001, 2000), (80, 400003, 300), (2, 1 << 23, 4000), (77, 70000, 5000)])
+def test_long_ranges_of_one_block(n, L, k):
+    """Many positions to each block: one block to a request, or several with
+    half a million each; heavy positions only here and there, in the first and
+    the last places among them."""
+    w = heavy_tailed(n, L, L + k)
+    w[:, 0], w[:, -9], w[:, L // 2] = 900.0, 901.0, 900.0
+    w[1, L // 3:2 * L // 3] = 0
+    assert torch.equal(select(w, None, k, 8).cpu(), want(w, [L] * n, k, 8))
+
+
 def test_many_equal_weights_at_the_border():
     """More equal weights than any list holds, on both sides of the border, and
     long rows of NaN and -infinity."""
