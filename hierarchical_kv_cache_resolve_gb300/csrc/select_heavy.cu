@@ -24,7 +24,7 @@
 // another twice, once for the maxima's counts and once for the lists.  With
 // more candidates than the lists hold (a large k) every CTA counts all its
 // keys instead, by 11, 11 and 10 bits.
-// Measured: 11.2 us for 32 requests of 32768 positions (clusters of 4; about
+// Measured: 11.1 us for 32 requests of 32768 positions (clusters of 4; about
 // ten steps of 0.5 to 1.3 us), 24.3 us for 8 of 2^20 (clusters of 12, 33.5 MB
 // read in 7 us).  Listed candidates copied by the CTAs from one another, not
 // written by their finders, which leaves memory to be kept until the others are
@@ -186,15 +186,22 @@ __global__ void __launch_bounds__(kSelThreads)
             }
         }
     };
-    // Calls f(key, position, whether it is one) for every element of the vectors
-    auto each = [&](int v, const float4 *x, auto f) {
+    // Calls f(key, position, whether it is one) for positions [from, to), kEach
+    // single weights' loads at a time: for what seldom runs, in little code.
+    auto each = [&](int from, int to, auto f) {
+#pragma unroll 1
+        for (int j0 = from; j0 < to; j0 += kEach * kSelThreads) {
+            float x[kEach];
 #pragma unroll
-        for (int u = 0; u < kEach; ++u) {
-            const int j = 4 * (v + u * kSelThreads) - off;
-            f(order_key(x[u].x), j, j >= 0 && j < size);
-            f(order_key(x[u].y), j + 1, j + 1 >= 0 && j + 1 < size);
-            f(order_key(x[u].z), j + 2, j + 2 >= 0 && j + 2 < size);
-            f(order_key(x[u].w), j + 3, j + 3 >= 0 && j + 3 < size);
+            for (int u = 0; u < kEach; ++u) {
+                const int j = j0 + u * kSelThreads + tid;
+                x[u] = j >= to ? -INFINITY : j + off < 4 * held ? vals[j + off] : __ldg(wc + j);
+            }
+#pragma unroll
+            for (int u = 0; u < kEach; ++u) {
+                const int j = j0 + u * kSelThreads + tid;
+                f(order_key(x[u]), j, j < to);
+            }
         }
     };
 
@@ -203,6 +210,7 @@ __global__ void __launch_bounds__(kSelThreads)
     if (tid == 0) found[0] = my_top = n_list = 0;
     float4 top = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
     float row_top = -INFINITY;   // of the warp's rows of 32 vectors lane, lane + 32, ...
+#pragma unroll 1
     for (int v0 = 0; v0 < nv; v0 += kEach * kSelThreads) {
         float4 x[kEach];
         at(v0 + tid, 0, x);
@@ -240,9 +248,11 @@ __global__ void __launch_bounds__(kSelThreads)
     cluster.barrier_wait();
     // adds this CTA's counts to every CTA's sums
     auto add_counts = [&]() {
+#pragma unroll 1
         for (int b = tid; b < kBins; b += kSelThreads) {
             const uint32_t c = hist[b];
             if (c)
+#pragma unroll 4
                 for (int t = 0; t < ctas; ++t) atomicAdd(cluster.map_shared_rank(sums, t) + b, c);
             hist[b] = 0;
         }
@@ -259,6 +269,7 @@ __global__ void __launch_bounds__(kSelThreads)
     const float fb = __uint_as_float(B & 0x80000000u ? B ^ 0x80000000u : ~B);
     // the warp's rows that have any
     const uint32_t rows = __ballot_sync(0xFFFFFFFFu, every || row_top > fb);
+#pragma unroll 1
     for (int v0 = 0; v0 < nv; v0 += kEach * kSelThreads) {
         const uint32_t here = rows >> v0 / kSelThreads % 32;  // kEach divides 32
         if (!(here & ((1u << kEach) - 1u))) continue;
@@ -301,6 +312,7 @@ __global__ void __launch_bounds__(kSelThreads)
     const int per = kSelWarps / ctas, other = warp / per, first = (warp - other * per) * 32;
     if (other < ctas && other != rank && n_list <= (uint32_t)list_max) {
         uint32_t *dst = cluster.map_shared_rank(list, other);
+#pragma unroll 1
         for (int j = first + lane; j < (int)n_list; j += per * 32) dst[j] = list[j];
     }
     if (tid < ctas) {
@@ -311,6 +323,7 @@ __global__ void __launch_bounds__(kSelThreads)
     uint64_t candidates = 0;
     uint32_t highest = 0;
     bool listed = true;                     // the lists hold all candidates
+#pragma unroll 4
     for (int c = 0; c < ctas; ++c) {
         candidates += list_counts[c];
         highest = max(highest, tops[c]);
@@ -332,6 +345,7 @@ __global__ void __launch_bounds__(kSelThreads)
         need = want;
         int shift = max(0, 32 - __clz(highest - B) - 11);
         while (true) {
+#pragma unroll 1
             for (int j0 = first; j0 < total; j0 += per * 32) {
                 const uint32_t x = j0 + lane < total ? keys[j0 + lane] : 0u;
                 const uint32_t bin = (x - base) >> shift;
@@ -357,6 +371,7 @@ __global__ void __launch_bounds__(kSelThreads)
         }
         if (shift > 0) {
             // at most 32 keys in the bin, each ranked by a warp
+#pragma unroll 1
             for (int j = first + lane; j < total; j += per * 32) {
                 const uint32_t x = keys[j];
                 if (x >= base && (x - base) >> shift == 0) few[atomicAdd(&n_few, 1u)] = x;
@@ -379,6 +394,7 @@ __global__ void __launch_bounds__(kSelThreads)
             T = base;
         }
         if (other < rank)
+#pragma unroll 1
             for (int j = first + lane; j < total; j += per * 32) {
                 gt0 += keys[j] > T;
                 eq0 += keys[j] == T;
@@ -387,17 +403,14 @@ __global__ void __launch_bounds__(kSelThreads)
         if (candidates >= want) {
             uint32_t prefix = 0;
             need = want;
+#pragma unroll 1
             for (int pass = 0; pass < 3; ++pass) {
                 const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
                 const int bits = pass == 2 ? 10 : 11;
-                for (int v0 = 0; v0 < nv; v0 += kEach * kSelThreads) {
-                    float4 x[kEach];
-                    at(v0 + tid, held, x);
-                    each(v0 + tid, x, [&](uint32_t key, int, bool is) {
-                        count(hist, key, shift, (1u << bits) - 1u,
-                              is && (pass == 0 || key >> (shift + bits) == prefix), lane);
-                    });
-                }
+                each(0, size, [&](uint32_t key, int, bool is) {
+                    count(hist, key, shift, (1u << bits) - 1u,
+                          is && (pass == 0 || key >> (shift + bits) == prefix), lane);
+                });
                 __syncthreads();
                 add_counts();
                 cluster.sync();
@@ -410,14 +423,10 @@ __global__ void __launch_bounds__(kSelThreads)
         }
         // kept and equal ones of every CTA
         uint32_t n_gt = 0, n_eq = 0;
-        for (int v0 = 0; v0 < nv; v0 += kEach * kSelThreads) {
-            float4 x[kEach];
-            at(v0 + tid, held, x);
-            each(v0 + tid, x, [&](uint32_t key, int, bool is) {
-                n_gt += is && key > T;
-                n_eq += is && key == T;
-            });
-        }
+        each(0, size, [&](uint32_t key, int, bool is) {
+            n_gt += is && key > T;
+            n_eq += is && key == T;
+        });
         if (tid < 2) totals[tid][rank] = 0;
         __syncthreads();
         n_gt = __reduce_add_sync(0xFFFFFFFFu, n_gt);
@@ -452,17 +461,13 @@ __global__ void __launch_bounds__(kSelThreads)
             atomicOr((key > T ? gt_bits : eq_bits) + (j >> 5), 1u << (j & 31));
         };
         if (from_list) {
+#pragma unroll 1
             for (int j = tid; j < n_mine; j += kSelThreads)
                 mark(list[j], list_pos[j] - w0);
         } else {
-            // the vectors that reach into the window
-            for (int v0 = (w0 + off) / 4; 4 * v0 - off < w0 + w1; v0 += kEach * kSelThreads) {
-                float4 x[kEach];
-                at(v0 + tid, held, x);
-                each(v0 + tid, x, [&](uint32_t key, int j, bool is) {
-                    if (is) mark(key, j - w0);
-                });
-            }
+            each(w0, w0 + w1, [&](uint32_t key, int j, bool is) {
+                if (is) mark(key, j - w0);
+            });
         }
         const uint32_t g0 = __reduce_add_sync(0xFFFFFFFFu, gt0);
         const uint32_t q0 = __reduce_add_sync(0xFFFFFFFFu, eq0);
