@@ -460,8 +460,9 @@ int hs_sparse_attention(const void *d_q, const void *d_cache, int64_t cache_rows
 #define HS_ATTN_STATUS_TIMEOUT 0x1u
 
 /* Synchronises the device, then returns in *status and clears the
- * HS_ATTN_STATUS_* bits that hs_sparse_attention and hs_prefix_attention
- * calls have set on the current device since the last call (0: none).  Errors:
+ * HS_ATTN_STATUS_* bits that hs_sparse_attention, hs_prefix_attention and
+ * hs_sparse_attention_weights calls have set on the current device since the
+ * last call (0: none).  Errors:
  * HS_ERR_INVALID_ARG (status == NULL), HS_ERR_CUDA. */
 int hs_attention_status(uint32_t *status);
 
