@@ -691,7 +691,7 @@ int hs_select_heavy(const float *d_weights, int32_t weight_rows, int64_t n_posit
                     const int32_t *d_req_ids, const int32_t *d_len, int32_t n_req, int32_t k,
                     int32_t recent, int32_t *d_sel, void *stream) {
     if (!d_weights || !d_sel || weight_rows < 1 || n_positions < 1 || n_positions > INT32_MAX ||
-        n_req < 0 || n_req > 65535 || k < 1 || recent < 0 || recent > k ||
+        n_req < 0 || n_req > 65535 || k < 1 || k > kMaxRows || recent < 0 || recent > k ||
         misaligned4(d_weights) || misaligned4(d_req_ids) || misaligned4(d_len) ||
         misaligned4(d_sel))
         return HS_ERR_INVALID_ARG;

@@ -782,7 +782,7 @@ PrefixPlan prefix_plan(int n_req, int q_heads, int heads, int64_t prefix_len, in
     p.row_tiles = (int)((rows + kRows - 1) / kRows);
     const int keys = block_keys(p.row_tiles == 1);
     p.blocks = (int)((prefix_len + keys - 1) / keys);
-    p.total = heads * p.blocks;  // below 2^27
+    p.total = heads * p.blocks;  // at most 2^28
     const int pairs = (p.row_tiles + 1) / 2;
     const int most = heads * ((p.blocks + 1) / 2);
     // measured: a CTA's start and end at a head, and 128 keys of a pair of tiles

@@ -614,7 +614,8 @@ int hs_sparse_attention_weights(const void *d_q, const void *d_cache, int64_t ca
  * order, then -1 up to k: where n >= k it is a selection for hs_resolve.
  * d_weights, weight_rows, n_positions and d_req_ids as for
  * hs_sparse_attention_weights; an id outside [0, weight_rows) gives -1
- * throughout.  0 <= recent <= k.  d_weights is only read; 4-byte alignment.
+ * throughout.  0 <= recent <= k <= 2^30.  d_weights is only read; 4-byte
+ * alignment.
  * One kernel, no workspace; nothing is allocated; n_req == 0 enqueues
  * nothing; n_req <= 65535.  Errors: HS_ERR_INVALID_ARG, HS_ERR_CUDA.
  */

@@ -160,6 +160,12 @@ def test_select_heavy_refuses(lib, bad):
     assert _select(lib, **bad) == INVALID
 
 
+def test_select_heavy_refuses_a_k_whose_loops_would_pass_31_bits(lib):
+    assert _select(lib, k=1 << 30) == hs.HS_OK
+    assert _select(lib, k=(1 << 30) + 1) == INVALID
+    assert _select(lib, k=(1 << 31) - 1, recent=(1 << 31) - 1) == INVALID
+
+
 def test_select_heavy_accepts_an_empty_call(lib):
     assert _select(lib) == hs.HS_OK
     assert _select(lib, ids=None, lens=None) == hs.HS_OK
