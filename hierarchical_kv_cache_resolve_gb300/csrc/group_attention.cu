@@ -236,7 +236,7 @@ RowsPlan rows_plan(int n_req, int heads, int k, int ctas) {
 // How hs_prefix_attention shares the SMs out between the prefix and the
 // requests' own rows: so that both are done at about the same time, by what
 // they were measured to cost (in cycles): the prefix as its plan says; a tile
-// of 16 rows 1400 for each warp, and 2600 where the prefix is bound by HBM too
+// of 16 rows 1500 for each warp, and 2600 where the prefix is bound by HBM too
 // (one pair).
 void share_out(int n_req, int q_heads, int heads, int64_t prefix_len, int k, PrefixPlan *pp,
                RowsPlan *p) {
@@ -254,7 +254,7 @@ void share_out(int n_req, int q_heads, int heads, int64_t prefix_len, int k, Pre
         const int waves = (pp->groups * pairs + p->ctas + kSms - 1) / kSms;
         const double tx = waves * pp->cycles;
         const int turns = p->ctas * p->subs;
-        const double ty = (pairs > 1 ? 1400. : 2600.) * (double)((p->total + turns - 1) / turns);
+        const double ty = (pairs > 1 ? 1500. : 2600.) * (double)((p->total + turns - 1) / turns);
         *rows_last = ty > tx;
         return tx > ty ? tx : ty;
     };

@@ -24,10 +24,11 @@
 //             second product takes it from.
 // Pairs of tiles take blocks of 128 keys, and one warp issues the products of
 // both in turn: while one tile's softmax runs, the tensor core works on the
-// other's products.  (Measured at 512 queries to a head on 131072 keys: 237 us;
-// blocks of 64 keys with their scores in two buffers 280, as products of N = 64
-// read the queries from shared memory twice as often; a warp for each tile
-// 310; sixteen softmax warps, two threads to a row, 250.)
+// other's products.  (Measured at 512 queries to a head on 131072 keys beside
+// 2048 rows, the products then still issued under a branch: 237 us; blocks of
+// 64 keys with their scores in two buffers 280, as a product of N = 64 runs at
+// two thirds of the rate; a warp for each tile 310; sixteen softmax warps, two
+// threads to a row, 250.)
 // With a single tile of rows (few queries, bound by HBM and latency) the two
 // softmax groups take every other block of the same rows, each with a ring and
 // a product warp of its own, and the two results are joined in shared memory
@@ -35,11 +36,12 @@
 // the faster ones, as softmax and products of a short range overlap earlier:
 // 8.4 us against 9.7 at 517 keys, 16.8 against 18.8 at 57 queries on 20011.
 // The whole call measures 8.1 us at 2 requests of 8 heads on 517 keys and 33
-// rows, 16.3 at 57 queries to each of 4 heads on 20011 keys, 39.8 at 128
-// queries to each of 8 heads on 32768 keys and 512 rows (5.1 TB/s, 6.4 between
-// the start and the end) and 219 at 512 queries on 131072 keys and 2048 rows
-// (1.28 PFLOP/s; 1.51 without the rows: reads of shared memory bound it, 128
-// bytes a cycle for S = Q K^T alone).
+// rows, 16.4 at 57 queries to each of 4 heads on 20011 keys, 40 at 128 queries
+// to each of 8 heads on 32768 keys and 512 rows (5.0 TB/s, 6.4 between the start
+// and the end) and 210 to 219 at 512 queries on 131072 keys and 2048 rows (1.3
+// PFLOP/s beside 2.5 TB/s).  Without the rows the products take 2470 cycles for
+// 128 keys of a pair, of which the tensor pipe needs 2056, at the 1.57 to 1.75
+// GHz that power leaves: 1.58 PFLOP/s for the call.
 //
 // P is rounded once to bf16 (2^-8 of each probability, which averages out over
 // the keys to about the output's own rounding).  A second bf16 term for what
@@ -123,44 +125,54 @@ __device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lead) {
 constexpr uint32_t kIdesc = 1u << 4 | 1u << 7 | 1u << 10 | 128u >> 4 << 24;
 constexpr uint32_t kIdescV = kIdesc | 128u >> 3 << 17 | 1u << 16;  // N = 128
 
+// Products and arrivals are issued by the lane where `on` is not 0, by
+// predicate: a branch around them would leave the warp's uniform registers out
+// of use, and moving the operands there one by one took about as long as the
+// products (60 cycles each; 182 us for 174 at 512 queries to a head on 131072
+// keys).
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                       bool add) {
+                                       bool add, uint32_t on) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        "setp.ne.u32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add), "r"(on)
         : "memory");
 }
 
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
-                                       bool add) {
+                                       bool add, uint32_t on) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        "setp.ne.u32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add), "r"(on)
         : "memory");
 }
 
-// One lane of a converged warp, the same one every time.
-__device__ __forceinline__ bool elect_one() {
+// 1 in one lane of a converged warp, the same one every time.
+__device__ __forceinline__ uint32_t elect_one() {
     uint32_t r;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "elect.sync _|p, 0xFFFFFFFF;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(r));
-    return r != 0;
+    return r;
 }
 
 // `bar` gets an arrival once every product issued so far by this thread is done
-__device__ __forceinline__ void mma_commit(uint32_t bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                     bar)
-                 : "memory");
+__device__ __forceinline__ void mma_commit(uint32_t bar, uint32_t on) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.u32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+            bar),
+        "r"(on)
+        : "memory");
 }
-
 
 // 32 columns of this thread's TMEM lane; complete after tmem_wait_ld
 __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t *v) {
@@ -430,12 +442,17 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     } else if (warp == 9 || (kAlone && warp == 10)) {
         // ---- the products: the whole warp waits, one lane issues.  One warp
         // for a pair of tiles; with one tile, one for each group's blocks.
-        const int ring = warp - 9;
-        const bool issuer = elect_one();
+        const int ring = kAlone ? warp - 9 : 0;
+        const uint32_t issuer = elect_one();
         const uint64_t q_op = operand(s0 + kOffQ, 16);
         const uint64_t k_op = operand(s0 + kOffRing, 16), v_op = operand(s0 + kOffRing, kItemAtom);
         uint32_t p_phase = 0;               // bit 2 t + b: of p_ready(t, b)
         bool ok = true;
+        // the same answer in every lane, which keeps what follows uniform
+        auto wait = [&](uint32_t bar, uint32_t parity) {
+            return __all_sync(0xFFFFFFFFu, mbar_try(bar, parity)) ||
+                   __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort_flag));
+        };
         // the ring's items one after the other
         int at = kRing - 1;
         uint32_t round = 1;                 // its parity
@@ -445,26 +462,23 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                 round ^= 1;
             }
             const int slot = ring * kRing + at;
-            ok = mbar_wait(full(slot), round, abort_flag);
-            fence_after();
+            ok = wait(full(slot), round);
             return slot;
         };
         auto release = [&](int slot) {
-            if (issuer) mma_commit(empty(slot));
+            mma_commit(empty(slot), issuer);
         };
         // S_t = Q_t K^T into buffer b, 16 dimensions at a time
         auto scores = [&](int tile, int b, int slot) {
             const uint64_t q = q_op + (kAlone ? 0 : tile * (kTileBytes >> 4));
             const uint64_t k = k_op + slot * (kItemBytes >> 4);
-            if (issuer) {
 #pragma unroll
-                for (int c = 0; c < 8; ++c)
-                    mma_ss(tmem + tile * 128 + b * kKeys, q + (((c >> 2) * kAtom + (c & 3) * 32) >> 4),
-                           k + (((c >> 2) * kItemAtom + (c & 3) * 32) >> 4), kIdescS, c > 0);
-            }
+            for (int c = 0; c < 8; ++c)
+                mma_ss(tmem + tile * 128 + b * kKeys, q + (((c >> 2) * kAtom + (c & 3) * 32) >> 4),
+                       k + (((c >> 2) * kItemAtom + (c & 3) * 32) >> 4), kIdescS, c > 0, issuer);
         };
         auto signal = [&](int tile, int b) {
-            if (issuer) mma_commit(s_full(tile, b));
+            mma_commit(s_full(tile, b), issuer);
         };
         // O_t += P_t V, 16 keys at a time, each part of P as it is ready
         auto outputs = [&](int tile, int b, int slot, bool first) {
@@ -473,21 +487,19 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
 #pragma unroll
             for (int part = 0; part < kParts; ++part) {
                 const int bar = 2 * tile + b + part;
-                if (!(ok = mbar_wait(p_ready(tile, b + part), p_phase >> bar & 1u, abort_flag))) return false;
+                if (!(ok = wait(p_ready(tile, b + part), p_phase >> bar & 1u))) return false;
                 p_phase ^= 1u << bar;
                 fence_after();
-                if (issuer) {
 #pragma unroll
-                    for (int c = 4 * part; c < 4 * part + 4; ++c)
-                        mma_ts(d, pt + c * 8, v + c * (2048 >> 4), kIdescV, c > 0 || !first);
-                }
+                for (int c = 4 * part; c < 4 * part + 4; ++c)
+                    mma_ts(d, pt + c * 8, v + c * (2048 >> 4), kIdescV, c > 0 || !first, issuer);
             }
             return true;
         };
 #pragma unroll 1
         for (int head = head0; head <= head1 && ok; ++head) {
             const int n = count(head);
-            ok = mbar_wait(q_full, (head - head0) & 1, abort_flag);
+            ok = wait(q_full, (head - head0) & 1);
             fence_after();
             if constexpr (kAlone) {
                 // this group's blocks: every other.  The first scores into both
@@ -551,7 +563,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
             }
         }
         // no product may still run when the TMEM is given back
-        if (issuer) mma_commit(drained);
+        mma_commit(drained, issuer);
         mbar_drain(drained, 0);
     } else if (warp < 8) {
         // ---- softmax
@@ -785,14 +797,15 @@ PrefixPlan prefix_plan(int n_req, int q_heads, int heads, int64_t prefix_len, in
     p.total = heads * p.blocks;  // at most 2^28
     const int pairs = (p.row_tiles + 1) / 2;
     const int most = heads * ((p.blocks + 1) / 2);
-    // measured: a CTA's start and end at a head, and 128 keys of a pair of tiles
-    // (with one tile HBM takes as long)
-    // With the whole multiple where it pays: 48.1 -> 43.5 us at 128 queries to
-    // each of 8 heads on 32768 keys, 104 groups instead of 109.
+    // measured: a CTA's start and end at a head, and 128 keys of a pair of tiles,
+    // or of one (bound by HBM).  With the whole multiple where it pays: 48.1 ->
+    // 43.5 us at 128 queries to each of 8 heads on 32768 keys, 104 groups instead
+    // of 109.
+    const float block = (p.row_tiles == 1 ? 3000.f : 2500.f) / 128 * keys;
     auto cycles = [&](int groups) {
         const int longest = (p.total + groups - 1) / groups;
         const int heads_more = groups % heads == 0 ? 0 : (longest - 1) / p.blocks + 1;
-        return 13000.f * (1 + heads_more) + 3000.f / 128 * keys * longest;
+        return 13000.f * (1 + heads_more) + block * longest;
     };
     p.groups = ctas / pairs;
     if (p.groups > most) p.groups = most;
