@@ -71,6 +71,22 @@ def test_own_rows_alone(k):
     check(s, out)
 
 
+@pytest.mark.parametrize("P", [0, 300])
+@pytest.mark.parametrize("h", [1, 2, 3, 4, 5, 6, 7, 8])
+def test_long_selections_of_every_record_size(h, P):
+    """Ranges of rows many times as long as the ring that brings them, requests
+    that end inside a range, one row in five masked, one request without any."""
+    s = make(30, P, 4001, 3 * h, h, 500 + h)
+    s["idx"][torch.rand(s["idx"].shape, generator=s["g"], device="cuda") < 0.2] = -1
+    s["idx"][17] = s["rows"]
+    out = attend(s)
+    check(s, out, requests=[0, 1, 16, 18, 29] + ([17] if P else []))
+    if not P:
+        assert bool((out[17] == 0).all())
+    for _ in range(5):
+        assert torch.equal(attend(s).view(torch.int16), out.view(torch.int16))
+
+
 @pytest.mark.parametrize("h", [1, 2, 3, 4, 5, 6, 7, 8])
 @pytest.mark.parametrize("group", [1, 2, 3, 5, 8, 11, 16])
 def test_head_layouts(h, group):
