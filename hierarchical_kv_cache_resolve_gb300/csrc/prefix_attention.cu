@@ -35,7 +35,7 @@
 // behind the last block of a head.  Here blocks of 64 keys in two buffers are
 // the faster ones, as softmax and products of a short range overlap earlier:
 // 8.4 us against 9.7 at 517 keys, 16.8 against 18.8 at 57 queries on 20011.
-// The whole call measures 8.1 us at 2 requests of 8 heads on 517 keys and 33
+// The whole call measures 7.5 us at 2 requests of 8 heads on 517 keys and 33
 // rows, 16.4 at 57 queries to each of 4 heads on 20011 keys, 40 at 128 queries
 // to each of 8 heads on 32768 keys and 512 rows (5.0 TB/s, 6.4 between the start
 // and the end) and 210 to 219 at 512 queries on 131072 keys and 2048 rows (1.3
@@ -681,9 +681,9 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
             const int64_t part = (int64_t)(g + head) * n_rows + m_row;
             float *dst = p.o + part * kDim;
             asm volatile("" : "+l"(dst));  // computed here, not ahead of the loop over heads
-            if (!kAlone) {
+            if (!kAlone || n == 1) {  // (one block: group 0's)
 #pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
+                for (int c = 0; c < 4 && mine > 0; ++c) {
                     uint32_t o[32];
                     tmem_ld32(to + c * 32, o);
                     tmem_wait_ld<32>(o);
@@ -784,7 +784,7 @@ EncodeTiled encode_tiled() {
 
 // The prefix over at most `ctas` CTAs: as many groups of a CTA for every pair
 // of row tiles as fit (more CTAs than SMs run one behind the other), each at
-// two blocks or more (one for each softmax group).  A multiple of the heads
+// two blocks or more unless the prefix is short.  A multiple of the heads
 // where the longer ranges cost less than another start and end: no range then
 // reaches into a second head.
 PrefixPlan prefix_plan(int n_req, int q_heads, int heads, int64_t prefix_len, int ctas) {
@@ -796,7 +796,13 @@ PrefixPlan prefix_plan(int n_req, int q_heads, int heads, int64_t prefix_len, in
     p.blocks = (int)((prefix_len + keys - 1) / keys);
     p.total = heads * p.blocks;  // at most 2^28
     const int pairs = (p.row_tiles + 1) / 2;
-    const int most = heads * ((p.blocks + 1) / 2);
+    // A range of two blocks has one for each softmax group.  Ranges of one need
+    // no join of the groups, but are twice as many parts to merge: as long as
+    // those are what a few warps load at once (517 keys: 8.2 -> 7.5 us, 600 of
+    // pairs 13.8 -> 13.2; but 4000 keys 9.9 -> 10.4, 1100 of pairs 14.6 -> 15.2).
+    const int one_each = heads * p.blocks;
+    const bool single = one_each <= ctas / pairs && p.blocks <= (p.row_tiles == 1 ? 16 : 8);
+    const int most = single ? one_each : heads * ((p.blocks + 1) / 2);
     // measured: a CTA's start and end at a head, and 128 keys of a pair of tiles,
     // or of one (bound by HBM).  With the whole multiple where it pays: 48.1 ->
     // 43.5 us at 128 queries to each of 8 heads on 32768 keys, 104 groups instead
