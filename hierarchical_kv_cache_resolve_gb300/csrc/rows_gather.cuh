@@ -148,13 +148,7 @@ __device__ __forceinline__ void bring(const GroupArgs &a, const RowsPlan &p, int
         const uint32_t valid = __ballot_sync(0xFFFFFFFFu, use);
         if (n >= n_slots) {
             const bool ok = mbar_wait(empty(s0, slot), round ^ 1, abort_flag);
-            if (!__all_sync(0xFFFFFFFFu, ok)) {
-                // nothing may land after the CTA has left (in a normal run the
-                // other warps have waited for all of it): the slots' last tiles
-                for (int s = w; s < n_slots; s += warps)
-                    mbar_drain(full(s0, s), s < slot ? round : round ^ 1);
-                return;
-            }
+            if (!__all_sync(0xFFFFFFFFu, ok)) break;
             // zeros written here come before the copies
             if (zeroed >> slot & 1u) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             zeroed &= ~(1u << slot);
@@ -178,6 +172,9 @@ __device__ __forceinline__ void bring(const GroupArgs &a, const RowsPlan &p, int
         n += advance(slot);
         if (slot == w) round ^= 1;
     }
+    // nothing may land after the CTA has left: the slots' last tiles (one that
+    // had none has its wait for the phase before the first, which is over)
+    for (int s = w; s < n_slots; s += warps) mbar_drain(full(s0, s), s < slot ? round : round ^ 1);
 }
 
 __device__ __forceinline__ void ldsm_x4(uint32_t (&r)[4], uint32_t s) {
