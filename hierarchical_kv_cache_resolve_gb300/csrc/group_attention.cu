@@ -12,9 +12,9 @@
 // weights summed over the query heads, one thread per row: one addition per
 // position and call, so equal inputs give equal sums.
 //
-// Measured: hs_sparse_attention_weights 50.6 us for 32 requests of 2048 rows of
-// 4096 bytes and 32 query heads (rows 43 us at 6.2 TB/s, merge and weights 7),
-// 6.2 us for one request of 64 rows.
+// Measured: hs_sparse_attention_weights 51.6 us for 32 requests of 2048 rows of
+// 4096 bytes and 32 query heads (rows 43 us at 6.2 TB/s, merge and weights 8),
+// 5.4 us for one request of 64 rows.
 #include <cmath>
 #include <cstdint>
 
@@ -184,13 +184,29 @@ __global__ void __launch_bounds__(kMergeThreads)
     while (lanes < 32 && 2 * lanes * a.q_heads <= kMergeThreads) lanes *= 2;
     const int32_t req = a.req_ids ? a.req_ids[r] : r;
     const int32_t pos = j < a.k ? a.sel[(int64_t)r * a.k + j] : -1;
+    const bool live = j < a.k && req >= 0 && req < a.weight_rows && pos >= 0 && pos < a.n_positions;
+    const float *sc = a.scores + (int64_t)r * a.q_heads * a.k + j;
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    // With few blocks the first heads' scores are loaded while the maxima are on
+    // their way (1 x 64 rows 6.4 -> 5.5 us, 5 x 777 8.4 -> 7.3); with many the
+    // maxima would wait behind them (32 x 2048 50.9 -> 51.9).
+    constexpr int kFirst = 16;
+    float first[kFirst];
+    const int early = gridDim.x > kSms ? 0 : a.q_heads < kFirst ? a.q_heads : kFirst;
     {
         const int hq = threadIdx.x / lanes, turn = threadIdx.x % lanes;
         float M = -INFINITY, L = 0.f;
+        float2 next = make_float2(-INFINITY, 0.f);
+        const int n = hq < a.q_heads ? x.n : 0;
+        if (turn < n) next = p.ml[part_row(a, x, turn, r, hq)];
+        asm volatile("" ::: "memory");      // these first
+#pragma unroll
+        for (int u = 0; u < kFirst; ++u)
+            first[u] = live && u < early ? sc[(int64_t)u * a.k] : -INFINITY;
         if (hq < a.q_heads)
             for (int i = turn; i < x.n; i += lanes) {
-                const float2 ml = p.ml[part_row(a, x, i, r, hq)];
+                const float2 ml = next;
+                if (i + lanes < x.n) next = p.ml[part_row(a, x, i + lanes, r, hq)];
                 const float big = fmaxf(M, ml.x), base = big == -INFINITY ? 0.f : big;
                 L = L * exp2f(M - base) + ml.y * exp2f(ml.x - base);
                 M = big;
@@ -206,11 +222,13 @@ __global__ void __launch_bounds__(kMergeThreads)
             mi[hq] = make_float2(M == -INFINITY ? 0.f : M, L == 0.f ? 0.f : 1.f / L);
     }
     __syncthreads();
-    if (j >= a.k || req < 0 || req >= a.weight_rows || pos < 0 || pos >= a.n_positions) return;
-    const float *sc = a.scores + (int64_t)r * a.q_heads * a.k + j;
+    if (!live) return;
     float w = 0.f;
+#pragma unroll
+    for (int u = 0; u < kFirst; ++u)
+        if (u < early) w += exp2f(first[u] - mi[u].x) * mi[u].y;
 #pragma unroll 16
-    for (int hq = 0; hq < a.q_heads; ++hq)
+    for (int hq = early; hq < a.q_heads; ++hq)
         w += exp2f(sc[(int64_t)hq * a.k] - mi[hq].x) * mi[hq].y;
     // exactly one addition per position and call where positions differ
     if (w != 0.f) atomicAdd(a.weights + (int64_t)req * a.n_positions + pos, w);
