@@ -340,8 +340,8 @@ __global__ void __launch_bounds__(kSelThreads)
             for (int b = tid; b < 2 * kWords * kSelThreads; b += kSelThreads) dyn[b] = 0;
         const int total = other < ctas ? (int)list_counts[other] : 0;
         const uint32_t *keys = all + min(other, ctas - 1) * list_max;
-        // the need-th largest lies in [base, base + 2048 << shift)
-        uint32_t base = B;
+        // the need-th largest lies in the first `bins` bins of 1 << shift keys from base
+        uint32_t base = B, bins = kBins;
         need = want;
         int shift = max(0, 32 - __clz(highest - B) - 11);
         while (true) {
@@ -349,7 +349,7 @@ __global__ void __launch_bounds__(kSelThreads)
             for (int j0 = first; j0 < total; j0 += per * 32) {
                 const uint32_t x = j0 + lane < total ? keys[j0 + lane] : 0u;
                 const uint32_t bin = (x - base) >> shift;
-                const bool in = j0 + lane < total && x >= base && bin < kBins;
+                const bool in = j0 + lane < total && x >= base && bin < bins;
                 const uint32_t some = __ballot_sync(0xFFFFFFFFu, in);
                 if (!some) continue;
                 // many equal keys: the first lane's bin in one addition
@@ -366,6 +366,8 @@ __global__ void __launch_bounds__(kSelThreads)
             base += found[0] << shift;
             need = found[1];
             if (shift == 0 || found[2] <= 32) break;
+            // on within the bin found only: `need` no longer counts the keys above it
+            bins = 1u << min(shift, 11);
             shift = max(0, shift - 11);
             __syncthreads();                // every thread has read what was found
         }
