@@ -184,7 +184,10 @@ __global__ void __launch_bounds__(kMergeThreads)
     while (lanes < 32 && 2 * lanes * a.q_heads <= kMergeThreads) lanes *= 2;
     const int32_t req = a.req_ids ? a.req_ids[r] : r;
     const int32_t pos = j < a.k ? a.sel[(int64_t)r * a.k + j] : -1;
-    const bool live = j < a.k && req >= 0 && req < a.weight_rows && pos >= 0 && pos < a.n_positions;
+    // (a masked row's score alone would not do: 2^-inf times a NaN sum is NaN)
+    const int32_t row = j < a.k ? __ldg(a.idx + (int64_t)r * a.k + j) : -1;
+    const bool live = row >= 0 && (int64_t)row < a.cache_rows && req >= 0 && req < a.weight_rows &&
+                      pos >= 0 && pos < a.n_positions;
     const float *sc = a.scores + (int64_t)r * a.q_heads * a.k + j;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     // With few blocks the first heads' scores are loaded while the maxima are on
