@@ -640,8 +640,20 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                         }
                     }
                 }
-                const float shift = m == -INFINITY ? 0.f : -m;
-                const uint64_t scale2 = pair(__float_as_uint(scale), __float_as_uint(scale));
+                float factor = scale, shift = m == -INFINITY ? 0.f : -m;
+                // The maximum is rounded, the fused products below are not: what that
+                // rounding left, up to 1 here, is a power of two that P and l share, but
+                // from 2^31 on it would pass fp32's range.  There the scores are rounded
+                // as the maximum was.
+                if (__any_sync(0xFFFFFFFFu, fabsf(shift) > 0x1p24f)) {
+#pragma unroll
+                    for (int e = 0; e < kKeys; ++e)
+                        s[e] = __float_as_uint(
+                            __fadd_rn(__fmul_rn(__uint_as_float(s[e]), scale), shift));
+                    factor = 1.f;
+                    shift = 0.f;
+                }
+                const uint64_t scale2 = pair(__float_as_uint(factor), __float_as_uint(factor));
                 const uint64_t shift2 = pair(__float_as_uint(shift), __float_as_uint(shift));
                 uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
