@@ -617,8 +617,9 @@ int hs_prefix_attention(const void *d_q, const void *d_prefix, int64_t prefix_le
         misaligned16(d_out) || misaligned16(d_work) || (prefix_len > 0 && !d_prefix) ||
         misaligned16(d_prefix))
         return HS_ERR_INVALID_ARG;
-    if (k > 0 && (!d_cache || !d_idx || cache_rows < 1)) return HS_ERR_INVALID_ARG;
-    if (misaligned16(d_cache) || misaligned4(d_idx)) return HS_ERR_INVALID_ARG;
+    if (k > 0 && (!d_cache || !d_idx || cache_rows < 1 || misaligned16(d_cache) ||
+                  misaligned4(d_idx)))
+        return HS_ERR_INVALID_ARG;
     if (n_req == 0) return HS_OK;
     hs::PrefixPlan pp;
     hs::RowsPlan p;
