@@ -155,6 +155,25 @@ bool group_layout_ok(int32_t q_heads, int32_t heads) {
     return head_layout_ok(q_heads, heads) && q_heads % heads == 0 && q_heads / heads <= 16;
 }
 
+// x radians modulo one turn as a 64-bit fraction, to 2^-64; |x| < 2^53 turns.
+// In integers, as the error is multiplied by a position of up to 2^31: the 53
+// bits of a double, less those of the whole turns, leave too few.  (A few
+// multiplications for each of 64 frequencies: a division and a scaling call
+// took 3 us of the host's time.)
+uint64_t turn_fraction(double x) {
+    uint64_t bits;
+    std::memcpy(&bits, &x, sizeof bits);
+    int e = (int)(bits >> 52 & 0x7FF) - 1075;  // |x| = m * 2^e
+    uint64_t m = (bits & ((1ull << 52) - 1)) | 1ull << 52;
+    for (; e > 0; --e) m <<= 1;
+    if (e < -118) return 0;                    // below 2^-65 of a turn; subnormal numbers
+    // 1 / 2 pi in 128 bits; m / 2 pi with 64 bits of fraction, below 2^118
+    const unsigned __int128 t = (unsigned __int128)m * 0x28BE60DB9391054Aull +
+                                ((unsigned __int128)m * 0x7F09D5F47D4D3770ull >> 64);
+    const uint64_t f = (uint64_t)(e ? (t + ((unsigned __int128)1 << (-e - 1))) >> -e : t);
+    return x < 0 ? 0 - f : f;
+}
+
 }  // namespace
 
 static_assert(HS_STAMP_ENTRY == hs::S_ENTRY && HS_STAMP_LOADED == hs::S_LOADED &&
@@ -567,12 +586,9 @@ int hs_qk_norm_rope(const hs_qk_desc *desc, const void *d_q, const void *d_k, co
         misaligned4(d_pos) || (reinterpret_cast<uintptr_t>(d_rows) & 7u))
         return HS_ERR_INVALID_ARG;
     for (int i = 0; i < d.rot_dim / 2; ++i) {
-        // (multiplications only: a division and a scaling call for each of 64
-        // frequencies took 3 us of the host's time)
         const double turns = d.inv_freq[i] * 0.15915494309189533577;  // 1 / (2 pi)
         if (!(std::fabs(turns) < 9007199254740992.0)) return HS_ERR_INVALID_ARG;
-        const double frac = turns - std::floor(turns);  // [0, 1]; 1 where a tiny negative rounds up
-        a.freq[i] = frac < 1.0 ? (uint64_t)(frac * 18446744073709551616.0) : 0;  // 2^64
+        a.freq[i] = turn_fraction(d.inv_freq[i]);
     }
     if (n_tok == 0) return HS_OK;
     a.q = static_cast<const uint8_t *>(d_q);

@@ -9,9 +9,11 @@
 //
 // The angle.  pos * inv_freq in fp32 is off by a tenth of a radian at a
 // million positions.  The launch gives the frequency in turns as a 64-bit
-// fraction, inv_freq / 2 pi * 2^64, so the product with the position modulo
-// 2^64 -- one integer multiply -- is the angle's exact fraction of a turn;
-// its top 32 bits, as a signed fraction of half a turn, go to sincospif.
+// fraction, inv_freq / 2 pi * 2^64 to one unit, so the product with the position
+// modulo 2^64 -- one integer multiply -- is the angle's fraction of a turn, to
+// 2^-33 of one at any position.  Its top 32 bits, as a signed fraction of half a
+// turn, are rounded to fp32 (2^-25 of half a turn, which is what remains) and go
+// to sincospif.
 //
 // Bound by HBM: every head is read once and written once.  Eight lanes share
 // a head, two 16-byte chunks of it each, chosen so that both ends of every

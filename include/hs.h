@@ -503,7 +503,8 @@ typedef struct {
     /* elements from one token's first query / key / value head to the next
        token's: a multiple of 8, at least the heads' own width (0: exactly that) */
     int64_t q_stride, k_stride, v_stride;
-    /* inv_freq[i]: radians per position of pair i, i < rot_dim / 2 */
+    /* inv_freq[i]: radians per position of pair i, i < rot_dim / 2; less than
+       2^53 turns either way */
     double inv_freq[64];
 } hs_qk_desc;
 
@@ -528,9 +529,9 @@ typedef struct {
  *   r * L_ctx + pos.  A later launch in the same stream, an overlapping
  *   resolve too, reads what this call wrote; a record that the pool's slots
  *   already hold is not refreshed there.
- * fp32 throughout, one rounding to bf16 at the end; the angle is exact to
- * 2^-31 of half a turn at any position.  Outputs overlap no input.  All
- * buffers 16-byte aligned, d_pos 4, d_rows 8.  One kernel, no workspace;
+ * fp32 throughout, one rounding to bf16 at the end; the angle is within 2^-24
+ * of half a turn at any position and frequency.  Outputs overlap no input.
+ * All buffers 16-byte aligned, d_pos 4, d_rows 8.  One kernel, no workspace;
  * nothing is allocated; n_tok == 0 enqueues nothing.
  * Errors: HS_ERR_INVALID_ARG, HS_ERR_CUDA.
  */
