@@ -579,6 +579,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
             const int n = count(head), b0 = first_block(head);
             const int mine = n > first ? (n - first + step - 1) / step : 0;
             float m = -INFINITY, l = 0.f;
+            bool far = false;               // a maximum of the warp is past 2^24
 #pragma unroll 1
             for (int j = 0; j < mine && ok; ++j) {
                 const int buf = j & (kBufs - 1);
@@ -615,6 +616,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                     const float up = fmaxf(m, top);
                     const float f = m == -INFINITY ? 0.f : ex2(m - up);
                     m = up;
+                    far = __any_sync(0xFFFFFFFFu, m > -INFINITY && fabsf(m) > 0x1p24f);
                     l *= f;
                     if (j > 0) {
                         // the products on O so far are done: these scores came
@@ -640,21 +642,21 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                         }
                     }
                 }
-                float factor = scale, shift = m == -INFINITY ? 0.f : -m;
+                const float shift = m == -INFINITY ? 0.f : -m;
+                uint64_t scale2 = pair(__float_as_uint(scale), __float_as_uint(scale));
+                uint64_t shift2 = pair(__float_as_uint(shift), __float_as_uint(shift));
                 // The maximum is rounded, the fused products below are not: what that
                 // rounding left, up to 1 here, is a power of two that P and l share, but
                 // from 2^31 on it would pass fp32's range.  There the scores are rounded
                 // as the maximum was.
-                if (__any_sync(0xFFFFFFFFu, fabsf(shift) > 0x1p24f)) {
+                if (far) {
 #pragma unroll
                     for (int e = 0; e < kKeys; ++e)
                         s[e] = __float_as_uint(
                             __fadd_rn(__fmul_rn(__uint_as_float(s[e]), scale), shift));
-                    factor = 1.f;
-                    shift = 0.f;
+                    scale2 = 0x3F8000003F800000ull;  // (1, 1)
+                    shift2 = 0ull;
                 }
-                const uint64_t scale2 = pair(__float_as_uint(factor), __float_as_uint(factor));
-                const uint64_t shift2 = pair(__float_as_uint(shift), __float_as_uint(shift));
                 uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
                 for (int c = 0; c < kKeys / 32; ++c) {
