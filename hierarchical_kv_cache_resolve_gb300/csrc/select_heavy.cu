@@ -22,13 +22,18 @@
 // neighbours not even that where their maximum is no larger (three in four
 // with 2048 of a million wanted); and the CTAs wait for one
 // another twice, once for the maxima's counts and once for the lists.  With
-// more candidates than the lists hold (a large k) every CTA counts all its
-// keys instead, by 11, 11 and 10 bits.
-// Measured: 11.1 us for 32 requests of 32768 positions (clusters of 4; about
-// ten steps of 0.5 to 1.3 us), 24.3 us for 8 of 2^20 (clusters of 12, 33.5 MB
-// read in 7 us).  Listed candidates copied by the CTAs from one another, not
-// written by their finders, which leaves memory to be kept until the others are
-// done: 12.0 us; every weight compared: 26.4.
+// more candidates than the lists hold -- a large k, weights that lie within one
+// bin, heavy positions side by side in the range of one CTA -- every CTA counts
+// all its keys instead, by 11, 11 and 10 bits.
+// Measured, 2048 of independent heavy-tailed weights kept: 11.3 us for 32
+// requests of 32768 positions (clusters of 4; about ten steps of 0.5 to 1.3 us),
+// 22.8 to 24.3 us for 8 of 2^20 (clusters of 12, 33.5 MB read in 7 us).  Listed
+// candidates copied by the CTAs from one another, not written by their finders,
+// which leaves memory to be kept until the others are done: 12.0 us; every weight
+// compared: 26.4.  With all keys counted, for the 8: 126 us (the first 1000 and
+// the last 65536 positions heaviest), 131 (30000 kept), 136 (weights within 10^-4
+// of one another), 138 (falling steadily); the last three 31, 26.5 and 25.3 for
+// the 32.
 // The kept positions -- keys above T, and the first of those equal to it --
 // are marked in two bitmaps over the CTA's range, whose prefix sums give each
 // its place in ascending order.

@@ -560,13 +560,14 @@ size_t hs_prefix_attention_bytes(int32_t n_req, int32_t q_heads, int32_t heads,
  * d_work: hs_prefix_attention_bytes(...) bytes of device memory (NULL if
  * that is 0), written and read by this call only: two calls that may run at
  * once, captured ones too, need one each.  Buffers 16-byte aligned, d_idx 4.
- * Scores, maxima, sums and outputs are held in fp32; each probability is
- * rounded once to bf16 for its product with the value, and the output once.
- * The work split depends on the arguments and the device only, so equal
- * inputs give bit-identical outputs.  Nothing is allocated; n_req == 0
- * enqueues nothing; n_req <= 65535, prefix_len < 2^31, k <= 2^30.  A
- * pipeline wait that runs out of time (one second) makes the affected outputs
- * NaN and sets HS_ATTN_STATUS_TIMEOUT (hs_attention_status).
+ * Scores, maxima, sums and outputs are held in fp32.  For its product with the
+ * value, a probability of the prefix is rounded once to bf16 (2^-8 of it) and
+ * one of the own rows is the sum of two bf16 terms (2^-17); the output is
+ * rounded once.  The work split depends on the arguments only, so equal inputs
+ * give bit-identical outputs.  Nothing is allocated; n_req == 0 enqueues
+ * nothing; n_req <= 65535, prefix_len < 2^31, k <= 2^30.  A pipeline wait that
+ * runs out of time (one second) makes the affected outputs NaN and sets
+ * HS_ATTN_STATUS_TIMEOUT (hs_attention_status).
  * Errors: HS_ERR_INVALID_ARG (also a workspace that is too small),
  * HS_ERR_CUDA.
  */
@@ -617,6 +618,10 @@ int hs_sparse_attention_weights(const void *d_q, const void *d_cache, int64_t ca
  * hs_sparse_attention_weights; an id outside [0, weight_rows) gives -1
  * throughout.  0 <= recent <= k <= 2^30.  d_weights is only read; 4-byte
  * alignment.
+ * The time depends on the weights: a few candidates for the last place are
+ * sought first, and where one part of a request holds too many of them (heavy
+ * positions side by side, weights that lie close, a large k) all weights are
+ * counted instead, which takes two to six times as long.
  * One kernel, no workspace; nothing is allocated; n_req == 0 enqueues
  * nothing; n_req <= 65535.  Errors: HS_ERR_INVALID_ARG, HS_ERR_CUDA.
  */
