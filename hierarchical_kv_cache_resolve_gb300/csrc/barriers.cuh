@@ -64,7 +64,15 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity,
     return true;
 }
 
-// The same without regard to the flag: what must have ended before the CTA
+// The same for a converged warp: one answer for all its lanes, which go on
+// together (lanes leave the loop above one by one, and instructions that the
+// whole warp has to execute at once may follow).
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity,
+                                               volatile uint32_t *abort_flag) {
+    return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort_flag));
+}
+
+// mbar_wait without regard to the flag: what must have ended before the CTA
 // may reuse or leave its memory.
 __device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity) {
     const uint64_t t0 = globaltimer();

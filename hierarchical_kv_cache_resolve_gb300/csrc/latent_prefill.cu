@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
         // the same answer in every lane, which keeps what follows uniform
         auto wait = [&](uint32_t bar, uint32_t parity) {
             return __all_sync(0xFFFFFFFFu, mbar_try(bar, parity)) ||
-                   __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort_flag));
+                   mbar_wait_warp(bar, parity, abort_flag);
         };
         auto wait_piece = [&](int c) { return ok = wait(full(c % kPieces), (c / kPieces) & 1); };
         auto release = [&](int c) { mma_commit(empty(c % kPieces), issuer); };
@@ -312,10 +312,10 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
         const int me = tid - 320;
 #pragma unroll 1
         for (int j = partial; j < n; ++j) {
-            bool ok = mbar_wait(look, (j - partial) & 1, abort_flag);
+            bool ok = mbar_wait_warp(look, (j - partial) & 1, abort_flag);
             for (int h = 0; h < 2; ++h) {
                 const int c = 3 + 5 * j + h;
-                ok = ok && mbar_wait(full(c % kPieces), (c / kPieces) & 1, abort_flag);
+                ok = ok && mbar_wait_warp(full(c % kPieces), (c / kPieces) & 1, abort_flag);
             }
             if (!ok) break;
             // keys from the first that some query does not see: 16 bytes (dimensions
@@ -375,7 +375,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
         bool far = false;                   // a maximum of the warp is past 2^24
 #pragma unroll 1
         for (int j = 0; j < mine && ok; ++j) {
-            ok = __all_sync(0xFFFFFFFFu, mbar_wait(s_full(t), s_phase, abort_flag));
+            ok = mbar_wait_warp(s_full(t), s_phase, abort_flag);
             if (!ok) break;
             s_phase ^= 1u;
             fence_after();
@@ -458,10 +458,9 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
         }
         // every product on O done
         if (mine > 0 && ok) {
-            ok = mbar_wait(s_full(t), s_phase, abort_flag);
+            ok = mbar_wait_warp(s_full(t), s_phase, abort_flag);
             fence_after();
         }
-        ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok && lane == 0) atomicOr(&g_prefill_status, HS_ATTN_STATUS_TIMEOUT);
         // a query that sees nothing gets zeros
         const bool whole = a.splits == 1;
@@ -481,6 +480,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
             uint32_t o[32];
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] = 0u;
+            __syncwarp();                    // TMEM is read by whole warps
             if (mine > 0) {
                 tmem_ld32(to + c * 32, o);
                 tmem_wait_ld<32>(o);

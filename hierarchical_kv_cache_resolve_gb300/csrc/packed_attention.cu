@@ -478,7 +478,7 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 // the outputs that read these chunks
-                if (i > 0) ok = ok && mbar_wait(pv_done(c), (i - 1) & 1, abort_flag);
+                if (i > 0) ok = ok && mbar_wait_warp(pv_done(c), (i - 1) & 1, abort_flag);
 #pragma unroll
                 for (int p = 0; p < 2; ++p) {
                     const uint32_t lo = scales2(scales[p][c]), hi = scales2(scales[p][c] >> 16);
@@ -508,7 +508,7 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
             if (i + 1 < tiles) {
                 load_piece(0, 0);
                 load_piece(1, 0);
-                ok = ok && mbar_wait(p_ready, i & 1, abort_flag);
+                ok = ok && mbar_wait_warp(p_ready, i & 1, abort_flag);
 #pragma unroll
                 for (int c = 1; c < (kOwnP ? 2 : 3); ++c)
 #pragma unroll
@@ -531,7 +531,7 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
             // the same answer in every lane, which keeps what follows uniform
             auto wait = [&](uint32_t bar, uint32_t parity) {
                 return __all_sync(0xFFFFFFFFu, mbar_try(bar, parity)) ||
-                       __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort_flag));
+                       mbar_wait_warp(bar, parity, abort_flag);
             };
 #pragma unroll 1
             for (int i = 0; i < tiles && ok; ++i) {
@@ -588,7 +588,7 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
                 fill_masked();
                 load_four(i + 1);
                 const int b = i % kOthersChunks, turn = i / kOthersChunks;
-                if (turn > 0) ok = __all_sync(0xFFFFFFFFu, mbar_wait(others_free(b), (turn - 1) & 1, abort_flag));
+                if (turn > 0) ok = mbar_wait_warp(others_free(b), (turn - 1) & 1, abort_flag);
                 if (!ok) break;
                 bring_others(b);
                 done = i + 1;
@@ -643,7 +643,7 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
             asm volatile("" : "+r"(p_at));  // addresses formed here, not kept for the loop
             const bool valid = in_range(my_row);
             const int32_t next_row = load_index((i + 1) * kTileRows + row);
-            ok = ok && mbar_wait(s_full, i & 1, abort_flag);
+            ok = ok && mbar_wait_warp(s_full, i & 1, abort_flag);
             fence_after();
             // eight scores, of products that are there
             auto scores = [&](int c, const uint32_t *x, float *s) {
@@ -729,6 +729,7 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
                         }
                     }
                     if (lane < 8) top[w * kMaxN + h0 + c + lane] = s[0];
+                    __syncwarp();            // TMEM is read by whole warps
                 }
                 meet();
                 // the factors of what is there already; the new maxima
@@ -787,6 +788,7 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
                 if (lane == 0)
 #pragma unroll
                     for (int e = 0; e < 16; ++e) top[c + e] = __uint_as_float(x[e]);
+                __syncwarp();
             }
         }
         meet();
@@ -819,6 +821,7 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
             cluster.sync();                     // all chunks are free
             if (half == 0 && row < N)
                 for (int c = 0; c < nsplit; ++c) cluster.map_shared_rank(ml_s, c)[split * N + row] = mine;
+            __syncwarp();
 #pragma unroll 1
             for (int m = half; m < 4; m += 2) {
                 // dimensions [128 m + 32 w, ... + 32): a unit, [split][unit][four heads][dimension]
