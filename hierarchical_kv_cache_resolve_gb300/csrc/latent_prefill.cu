@@ -23,8 +23,10 @@
 //             see whole (below), while their scores are on their way.
 // While one tile's softmax runs, the tensor core works on the other's products.
 //
-// P is rounded once to bf16; the maximum only rises when a block exceeds it by
-// more than 2^8, as in prefix_attention.cu.
+// P is rounded once to bf16; a query's maximum only rises when a block exceeds it
+// by more than 2^8.  O is rescaled by the warp then, by 1 for the queries whose own
+// maximum stays: a key has no effect on the queries that do not see it, not even on
+// how their probabilities are rounded, and rows that see nothing ask for nothing.
 //
 // A masked key has P = 0, and 0 V must be 0 whatever V holds: rows behind the
 // sequence, which may be anything, are zeroed in shared memory, and so are
@@ -372,7 +374,6 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
         uint32_t s_phase = 0;
         bool ok = true;
         float m = -INFINITY, l = 0.f;
-        bool far = false;                   // a maximum of the warp is past 2^24
 #pragma unroll 1
         for (int j = 0; j < mine && ok; ++j) {
             ok = mbar_wait_warp(s_full(t), s_phase, abort_flag);
@@ -401,11 +402,12 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
                                      __uint_as_float(s[c * 32 + e + 2 * h + 1]));
             }
             const float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * scale;
-            if (__any_sync(0xFFFFFFFFu, top > m + kRise || m == -INFINITY)) {
-                const float up = fmaxf(m, top);
-                const float f = m == -INFINITY ? 0.f : ex2(m - up);
-                m = up;
-                far = __any_sync(0xFFFFFFFFu, m > -INFINITY && fabsf(m) > 0x1p24f);
+            // (false as long as a query has seen nothing, true at its first score)
+            const bool rise = top > m + kRise;
+            if (__any_sync(0xFFFFFFFFu, rise)) {
+                // each query by its own scores: what others see must not show in its bits
+                const float f = !rise ? 1.f : m == -INFINITY ? 0.f : ex2(m - top);
+                if (rise) m = top;
                 l *= f;
                 if (j > 0) {
                     // the products on O so far are done: these scores came behind them
@@ -427,13 +429,14 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
             // rounding left, up to 1 here, is a power of two that P and l share, but
             // from 2^31 on it would pass fp32's range.  There the scores are rounded
             // as the maximum was.
-            if (far) {
+            if (fabsf(shift) > 0x1p24f) {
 #pragma unroll
                 for (int e = 0; e < kKeys; ++e)
                     s[e] = __float_as_uint(__fadd_rn(__fmul_rn(__uint_as_float(s[e]), scale), shift));
                 scale2 = 0x3F8000003F800000ull;  // (1, 1)
                 shift2 = 0ull;
             }
+            __syncwarp();
             uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
             for (int c = 0; c < kKeys / 32; ++c) {
