@@ -775,7 +775,9 @@ size_t hs_latent_prefill_bytes(int32_t n_tok, int32_t n_keys, int32_t n_seq, int
  *   sequence are left as they were in d_out; n_tok and n_keys are the rows that
  *   d_q and d_out, and d_k, d_v and d_kr have.
  * Whatever a query does not see -- later keys, other sequences, rows behind the
- * last -- has no effect on it, infinities and NaN included.
+ * last -- has no effect on it, not on a single bit, infinities and NaN included.  An
+ * infinity or NaN among the values that it sees, however little they weigh, leaves
+ * that dimension of its output infinite or NaN.
  * d_work: hs_latent_prefill_bytes(...) bytes as for hs_prefix_attention.  Buffers
  * 16-byte aligned, starts 4; n_tok, n_keys <= 2^30, n_seq <= 65535, heads <= 128;
  * scale > 0 and finite.  Scores, maxima, sums and outputs are held in fp32; a
