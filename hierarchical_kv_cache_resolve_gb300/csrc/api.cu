@@ -876,7 +876,9 @@ int hs_packed_attention(const void *d_q, const void *d_cache, int64_t cache_rows
 }
 
 size_t hs_latent_prefill_bytes(int32_t n_tok, int32_t n_keys, int32_t n_seq, int32_t heads) {
-    if (n_tok < 1 || n_keys < 0 || n_seq < 1 || n_seq > 65535 || heads < 1 || heads > 128) return 0;
+    if (n_tok < 1 || n_tok > (1 << 30) || n_keys < 0 || n_keys > (1 << 30) || n_seq < 1 || n_seq > 65535 ||
+        heads < 1 || heads > 128)
+        return 0;
     return hs::latent_prefill_bytes(n_tok, n_keys, n_seq, heads);
 }
 
