@@ -729,6 +729,19 @@ bool misaligned8(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 7u) !
 
 constexpr int64_t kMaxStride = INT64_MAX >> 34;  // bytes of 2^31 tokens stay within 63 bits
 
+// Whether two of the pieces of 64 elements that n_tok tokens have of `heads` heads
+// share an element (strides of at least 64).
+bool pieces_overlap(int64_t n_tok, int64_t heads, int64_t token_stride, int64_t head_stride) {
+    if (token_stride >= (heads - 1) * head_stride + 64) return false;  // a token's lie together
+    for (int64_t h = 1; h < heads; ++h) {
+        // the nearest pieces of head 0 on either side
+        const int64_t at = h * head_stride, t = at / token_stride;
+        if ((t < n_tok && at - t * token_stride < 64) || (t + 1 < n_tok && (t + 1) * token_stride - at < 64))
+            return true;
+    }
+    return false;
+}
+
 bool records_ok(const void *from, const void *to, int64_t n, int32_t shift, int64_t packed_rows,
                 const int64_t *d_rows) {
     return from && to && !misaligned16(from) && !misaligned16(to) && !misaligned8(d_rows) && n >= 0 &&
@@ -784,6 +797,7 @@ int hs_latent_norm_rope(const hs_latent_desc *desc, const void *d_q, const void 
             if (heads[i] < 64 || heads[i] % 8 != 0 || tokens[i] < 64 ||
                 tokens[i] % 8 != 0 || tokens[i] > kMaxStride)
                 return HS_ERR_INVALID_ARG;
+    if (pieces_overlap(n_tok, d.q_heads, tokens[1], heads[1])) return HS_ERR_INVALID_ARG;
     if (kv_stride < 576 || kv_stride % 8 != 0 || kv_stride > kMaxStride) return HS_ERR_INVALID_ARG;
     if ((d.q_heads > 0 && (!d_q || !d_q_out)) || !d_kv || !d_pos || !d_records || misaligned16(d_q) ||
         misaligned16(d_q_out) || misaligned16(d_kv) || misaligned16(d_w) || misaligned16(d_records) ||

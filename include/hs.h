@@ -669,7 +669,7 @@ typedef struct {
     float magnitude;      /* factor of the rotated dimensions (usually 1) */
     /* elements from a token's, or a head's, first rotating dimension to the
        next one's: multiples of 8, at least 64 (0: q_heads * head stride, 64);
-       of the output likewise */
+       of the output likewise, where no two heads may share an element */
     int64_t q_stride, q_head_stride, out_stride, out_head_stride;
     int64_t kv_stride;    /* between tokens of d_kv: a multiple of 8, >= 576 (0: 576) */
     /* inv_freq[i]: radians per position of pair i; less than 2^53 turns */
