@@ -799,8 +799,9 @@ int hs_latent_norm_rope(const hs_latent_desc *desc, const void *d_q, const void 
                 return HS_ERR_INVALID_ARG;
     if (pieces_overlap(n_tok, d.q_heads, tokens[1], heads[1])) return HS_ERR_INVALID_ARG;
     if (kv_stride < 576 || kv_stride % 8 != 0 || kv_stride > kMaxStride) return HS_ERR_INVALID_ARG;
-    if ((d.q_heads > 0 && (!d_q || !d_q_out)) || !d_kv || !d_pos || !d_records || misaligned16(d_q) ||
-        misaligned16(d_q_out) || misaligned16(d_kv) || misaligned16(d_w) || misaligned16(d_records) ||
+    if (d.q_heads > 0 && (!d_q || !d_q_out || misaligned16(d_q) || misaligned16(d_q_out)))
+        return HS_ERR_INVALID_ARG;
+    if (!d_kv || !d_pos || !d_records || misaligned16(d_kv) || misaligned16(d_w) || misaligned16(d_records) ||
         misaligned4(d_pos) || misaligned8(d_rows))
         return HS_ERR_INVALID_ARG;
     for (int i = 0; i < 32; ++i) {
@@ -914,9 +915,10 @@ int hs_latent_prefill(const void *d_q, const void *d_k, const void *d_v, const v
     if (kv_stride < width || kv_stride % 8 != 0 || kv_stride > (1ll << 38) || kr_stride < 64 ||
         kr_stride % 8 != 0 || kr_stride > (1ll << 38))
         return HS_ERR_INVALID_ARG;
-    if (!d_q || !d_q_starts || !d_k_starts || !d_out || (n_keys > 0 && (!d_k || !d_v || !d_kr)) ||
-        misaligned16(d_q) || misaligned16(d_k) || misaligned16(d_v) || misaligned16(d_kr) ||
-        misaligned16(d_out) || misaligned16(d_work) || misaligned4(d_q_starts) || misaligned4(d_k_starts))
+    if (!d_q || !d_q_starts || !d_k_starts || !d_out || misaligned16(d_q) || misaligned16(d_out) ||
+        misaligned16(d_work) || misaligned4(d_q_starts) || misaligned4(d_k_starts))
+        return HS_ERR_INVALID_ARG;
+    if (n_keys > 0 && (!d_k || !d_v || !d_kr || misaligned16(d_k) || misaligned16(d_v) || misaligned16(d_kr)))
         return HS_ERR_INVALID_ARG;
     const size_t need = hs_latent_prefill_bytes(n_tok, n_keys, n_seq, heads);
     if (need > work_bytes || (need && !d_work)) return HS_ERR_INVALID_ARG;

@@ -685,6 +685,7 @@ typedef struct {
  * d_q, d_q_out: the first rotating dimension of token 0's head 0 (bf16), wherever
  *   the heads lie: the last 64 of 192 dimensions that hs_latent_prefill takes, or
  *   of the 576 that the decode calls take.  Nothing else of them is touched.
+ *   Ignored if q_heads is 0.
  *   d_q_out may be d_q with the same strides; outputs overlap no input otherwise.
  * d_pos: device int32[n_tok], any value.
  * d_records: record_rows rows of 1152 or 416 bytes; d_rows, rows outside the
@@ -769,7 +770,8 @@ size_t hs_latent_prefill_bytes(int32_t n_tok, int32_t n_keys, int32_t n_seq, int
  * d_k, d_v: bf16, head h of key j at element j * kv_stride + h * kv_head_stride
  *   of each (0: heads * kv_head_stride, 128); they may be parts of one expansion's
  *   output.  d_kr: bf16, key j's 64 at element j * kr_stride (0: 64), for instance
- *   in the bf16 records (d_records + 512, 576).  Strides are multiples of 8.
+ *   in the bf16 records (d_records + 512, 576).  Strides are multiples of 8.  The
+ *   three buffers are ignored if n_keys is 0.
  * d_q_starts, d_k_starts: device int32[n_seq + 1], not decreasing; entries outside
  *   [0, n_tok] and [0, n_keys] are taken to the nearer end.  Queries of no
  *   sequence are left as they were in d_out; n_tok and n_keys are the rows that

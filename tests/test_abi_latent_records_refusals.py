@@ -58,3 +58,18 @@ def test_overlap_is_exact():
             for token in range(64, 700, 8):
                 for head in (64, 72, 128, 200, 320, 576, 640):
                     assert rule(n, h, token, head) == overlaps(n, h, token, head), (n, h, token, head)
+
+
+@pytest.mark.parametrize("q,q_out", [(None, None), (4100, 20484), (1, 3)])
+def test_query_buffers_are_ignored_without_query_heads(lib, q, q_out):
+    assert _rope(lib, hs.latent_desc(0, FREQ), q=q, q_out=q_out) == hs.HS_OK
+    assert _rope(lib, hs.latent_desc(1, FREQ), q=q, q_out=q_out) == INVALID
+
+
+@pytest.mark.parametrize("k", [None, 4100, 1])
+def test_key_buffers_are_ignored_without_keys(lib, k):
+    def call(keys):
+        return lib.hs_latent_prefill(4096, k, k, k, 0, 0, 0, 20480, 24576, 2, 0, keys, 16, 0.1, 28672, 32768, 1 << 40,
+                                     None)
+    assert call(0) == hs.HS_OK
+    assert call(1) == INVALID
