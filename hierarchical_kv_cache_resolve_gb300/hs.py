@@ -333,7 +333,8 @@ def hs_rope_frequencies(rot_dim: int, base: float = 10000.0, factor: float = 1.0
                         trained: int = 4096, fast: float = 32.0, slow: float = 1.0):
     """(inv_freq, magnitude) of a rotation of rot_dim dimensions for contexts
     `factor` times as long as the `trained` one: fast pairs as they are, slow
-    ones slowed down, those between in parts."""
+    ones slowed down, those between in parts.  The attention's scale is to be
+    multiplied by magnitude ** 2."""
     freq, magnitude = (ctypes.c_double * 64)(), ctypes.c_double()
     _check(_lib().hs_rope_frequencies(rot_dim, base, factor, trained, fast, slow, freq,
                                       ctypes.byref(magnitude)), "hs_rope_frequencies")

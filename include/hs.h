@@ -650,10 +650,13 @@ int hs_select_heavy(const float *d_weights, int32_t weight_rows, int64_t n_posit
  * f = base^(-2i / rot_dim), pairs that turn `fast` times or more within the
  * `trained` positions keep f, those that turn `slow` times or less get
  * f / factor, and the pairs between a mean of the two that moves evenly over
- * them (their ends rounded outwards to whole pairs).  inv_freq (host
- * double[rot_dim / 2]) and, unless NULL, *magnitude = 0.1 ln(factor) + 1, the
- * factor of the rotated dimensions, fill hs_qk_desc and hs_latent_desc.  With
- * factor 1 they are f and 1.  Usual: fast 32, slow 1.  Host only.
+ * them (their ends rounded outwards to whole pairs, within pair 0 and
+ * rot_dim - 1).  inv_freq (host double[rot_dim / 2]) fills hs_qk_desc or
+ * hs_latent_desc.  *magnitude (unless NULL) = 0.1 ln(factor) + 1 is for the
+ * softmax: queries and keys are taken this much larger, so every score gets its
+ * square, which the caller puts into the attention's scale.  It is no factor of
+ * the rotation: of a latent record 64 of 576 dimensions turn.  With factor 1 they
+ * are f and 1.  Usual: fast 32, slow 1.  Host only.
  * Errors: HS_ERR_INVALID_ARG.
  */
 int hs_rope_frequencies(int32_t rot_dim, double base, double factor, int64_t trained,
@@ -666,7 +669,8 @@ typedef struct {
     int32_t packed;       /* records: 0 bf16 (1152 bytes), 1 packed (416 bytes) */
     int32_t shift;        /* of packed records */
     float eps;            /* >= 0 */
-    float magnitude;      /* factor of the rotated dimensions (usually 1) */
+    float magnitude;      /* factor of the rotated dimensions alone: 1 but for models
+                             whose definition has one there */
     /* elements from a token's, or a head's, first rotating dimension to the
        next one's: multiples of 8, at least 64 (0: q_heads * head stride, 64);
        of the output likewise, where no two heads may share an element */

@@ -83,3 +83,28 @@ def run_example():
 def test_the_example_runs_with_buffers_that_are_large_enough():
     x, _ = run_example()
     assert bool(torch.isfinite(x["o_prompt"]).all()) and bool(torch.isfinite(x["o"]).all())
+
+
+def test_the_example_agrees_with_the_definition():
+    x, given = run_example()
+    freq, _ = hs.hs_rope_frequencies(64, 10000.0, FACTOR, 4096)
+    scale = 192 ** -0.5 * (0.1 * math.log(FACTOR) + 1) ** 2
+    turned = ref.turned(given[..., 128:], x["pos"], freq, 1.0, True)[0]
+    assert torch.equal(x["q"][..., :128], given[..., :128])
+    assert bool(((x["q"][..., 128:].double() - turned).abs() <= ref.BF16 * turned.abs() + 2.0 ** -15).all())
+    rec, wide = x["rec"], x["wide"]
+    shared = ref.turned(x["kv"][:, None, 512:], x["pos"], freq, 1.0, True)[0][:, 0]
+    assert bool(((rec[:, 512:].double() - shared).abs() <= ref.BF16 * shared.abs() + 2.0 ** -15).all())
+    for r in range(R):
+        of = slice(r * N, (r + 1) * N)
+        for i in (0, 1, N // 2, N - 1):
+            seen = slice(r * N, r * N + i + 1)
+            for head in (0, H - 1):
+                want, bound = ref.attention(x["q"][r * N + i, head][None],
+                                            torch.cat((wide[seen, head, :128], rec[seen, 512:]), 1),
+                                            wide[seen, head, 128:], scale, ref.BF16)
+                assert bool(((x["o_prompt"][r * N + i, head].double() - want[0]).abs() <= bound[0]).all())
+        keys = rec[of][x["sel"][r].long()]
+        want, bound = ref.attention(x["q_latent"][r], keys, keys[:, :512], scale,
+                                    torch.finfo(torch.float16).eps / 2, 2.0 ** -32)
+        assert bool(((x["o"][r].double() - want).abs() <= bound).all())
