@@ -60,8 +60,8 @@
 // when a row exceeds it by 2^8, for the eight heads around: only then are maxima
 // formed over the rows and O rescaled (32 x 2048 rows at 128 heads 42.4 us, 44.1 for
 // all heads at once).  P is rounded to f16 with 2^7 as its unit (so at most 2^15):
-// 2^-12 of a probability down to 2^-21, and 2^-32 below.  Scores, maxima, sums and
-// outputs are fp32.
+// half a step is 2^-11 of a probability down to 2^-21, and 2^-32 below.  Scores,
+// maxima, sums and outputs are fp32.
 //
 // The sums come from the products too, as ones times P^T: that keeps them out of
 // the softmax's registers, which hold no score longer than its P takes.

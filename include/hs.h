@@ -743,12 +743,13 @@ size_t hs_packed_attention_bytes(int32_t n_req, int32_t heads, int32_t k);
  * for hs_prefix_attention.  Buffers 16-byte aligned, d_idx 4; n_req <= 65535,
  * k <= 2^30.
  * Scores, maxima, sums and outputs are held in fp32 over exact values; a
- * probability is rounded once to f16 (2^-12 of it, 2^-32 at least) for its
- * product with the value and for the sum, and the output once.  A row whose score
- * is -inf weighs nothing; a request with no others gets zeros.  The work split
- * depends on the arguments and the device only, so equal inputs give bit-identical
- * outputs.
- * Nothing is allocated; n_req == 0 enqueues nothing.  A pipeline wait that runs
+ * probability is rounded once to f16 (2^-11 of it, 2^-32 at least) for its
+ * product with the value and for the sum, and the output once.  (The values are
+ * exact unless a head's last 64 dimensions exceed its others by 2^80 * 2^shift or
+ * more, and nothing overflows before the score itself while the rows' last 64 stay
+ * below 2^40.)  A row whose score is -inf weighs nothing; a request with no others
+ * gets zeros.  The work split depends on the arguments and the device only, so equal
+ * inputs give bit-identical outputs.  Nothing is allocated; n_req == 0 enqueues nothing.  A pipeline wait that runs
  * out of time (one second) makes the affected outputs NaN and sets
  * HS_ATTN_STATUS_TIMEOUT (hs_attention_status).
  * Errors: HS_ERR_INVALID_ARG, HS_ERR_CUDA.
