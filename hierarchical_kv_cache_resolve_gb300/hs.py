@@ -381,7 +381,7 @@ def hs_unpack_records(packed, packed_rows, shift, records, n, rows=None, stream=
 
 
 def hs_packed_attention_bytes(n_req: int, heads: int, k: int) -> int:
-    """Workspace bytes of hs_packed_attention (0: none needed)."""
+    """Workspace bytes of hs_packed_attention (0 so far: none needed)."""
     return int(_lib().hs_packed_attention_bytes(n_req, heads, k))
 
 

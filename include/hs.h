@@ -727,8 +727,8 @@ int hs_pack_records(const void *d_records, int64_t n, int32_t shift, void *d_pac
 int hs_unpack_records(const void *d_packed, int64_t packed_rows, int32_t shift, void *d_records,
                       int64_t n, const int64_t *d_rows, void *stream);
 
-/* Workspace bytes of hs_packed_attention, the same on every device (0: none
- * needed, or arguments that the call refuses). */
+/* Workspace bytes of hs_packed_attention: 0, its parts are joined on the chip.  A
+ * caller that asks goes on working where that changes. */
 size_t hs_packed_attention_bytes(int32_t n_req, int32_t heads, int32_t k);
 
 /*
@@ -740,8 +740,8 @@ size_t hs_packed_attention_bytes(int32_t n_req, int32_t heads, int32_t k);
  * d_idx: device int32 [n_req][k] (an index outside [0, cache_rows) masks its
  * row); d_out: device bf16 [n_req][heads][512].  A request with every row masked
  * gets zeros.  scale is finite.  d_work: hs_packed_attention_bytes(...) bytes as
- * for hs_prefix_attention.  Buffers 16-byte aligned, d_idx 4; n_req <= 65535,
- * k <= 2^30.
+ * for hs_prefix_attention (none: NULL; what is passed is not touched).  Buffers
+ * 16-byte aligned, d_idx 4; n_req <= 65535, 1 <= k <= 2^30.
  * Scores, maxima, sums and outputs are held in fp32 over exact values; a
  * probability is rounded once to f16 (2^-11 of it, 2^-32 at least) for its
  * product with the value and for the sum, and the output once.  (The values are
