@@ -35,11 +35,13 @@
 // heads 51.4 us, 45.0 without).
 //
 // Measured: 64 x 2048 rows at 16 heads 28.2 us, at 32 heads 32.2; 32 x 2048 at 128
-// heads 42.4.  At 16 heads a tile takes 2.5 us: 2.2 would be its 68 products if an
-// operand of 128 x 16 keeps each at the 64 cycles of a full one, which fits what was
-// seen of them, beside 147 KB written to shared memory as f16.  At 64 heads a tile
-// takes 3.6: scores 0.7 behind the last rows, softmax 0.9, outputs and the next rows
-// 2, which there is no room to overlap: a second tile does not fit.  Start and join
+// heads 42.4.  At 16 heads a tile takes 2.5 us, of which its loads are about half a
+// microsecond (all rows from cache: 23.7 us a call, 27.0 at 32 heads); a loop of the
+// loads alone takes 2.2 a tile.  What bounds the rest, 147 KB written to shared
+// memory as f16 or the 68 products (2.1 to 2.2 if an operand of 128 x 16 keeps each
+// at the 64 cycles of a full one, which was not measured), is not known.  At 64 heads
+// a tile takes 3.6: scores 0.7 behind the last rows, softmax 0.9, outputs and the next
+// rows 2, one after the other: a second tile of 128 rows does not fit.  Start and join
 // take 8 us of a call, 11 at 128 heads.
 // Other ways, 64 x 2048 at 16 heads and 32 x 2048 at 128: warp-level products on
 // the 4-bit rows in registers, whose conversions keep an MMA at 12 cycles instead
